@@ -313,6 +313,115 @@ mxf_status mxfp8_dispatch_quantize(const mxf_mlp_desc* desc /* host */, const in
                                    const void* x_tokens, int64_t tokens, int32_t topk, void* saved,
                                    void* workspace, void* stream);
 
+/* ------------------------------------------------------------------ layer norm */
+
+/* Layer norm over the rows of a row-major matrix, and its gradients:
+ *   mean = sum x / cols, var = sum (x - mean)^2 / cols, rstd = 1 / sqrt(var + eps),
+ *   xh = (x - mean) rstd, y = xh weight + bias;
+ *   g = dy weight, dx = rstd (g - sum g / cols - xh sum(g xh) / cols),
+ *   dweight = sum over rows of dy xh, dbias = sum over rows of dy.
+ * Statistics, sums and the two weight gradients are FP32 whatever the element type; y and dx are
+ * rounded once. A row that holds a NaN or an infinity gets NaN in y (and in its checkpoint) and
+ * touches no other row. */
+#define MXF_NORM_F32 1u         /* x, y, dy, dx are FP32 instead of BF16 */
+#define MXF_NORM_WEIGHT_F32 2u  /* weight and bias are FP32 instead of BF16 */
+
+typedef struct {
+  int64_t rows;    /* >= 0 */
+  int64_t cols;    /* 1 .. 2^20 */
+  int64_t ldx;     /* elements between rows of x, >= cols */
+  int64_t ldy;     /* elements between rows of y (forward) or dy (backward), >= cols */
+  int64_t lddx;    /* elements between rows of dx, >= cols (backward only) */
+  float eps;       /* >= 0 */
+  uint32_t flags;  /* MXF_NORM_F32 | MXF_NORM_WEIGHT_F32 */
+} mxf_norm_desc;
+
+/* Forward. weight and bias [cols] may be NULL (1 and 0); mean and rstd [rows] FP32 may be NULL.
+ * ckpt_q, ckpt_s: NULL, or the 8-bit checkpoint of xh for mxf_layer_norm_bwd: codes [rows, cols] and
+ * scales [rows, ceil(cols / 32)], dense, equal to the row-wise MXFP8 of xh rounded to BF16 (groups of
+ * 32 along the row, the last one short where cols % 32 != 0; read back by mxfp8_dequantize).
+ * Pointers need the alignment of their elements (codes and scales: none); 16-byte alignment of rows
+ * is faster. y may be x. rows = 0 is a no-op that accepts NULL pointers.
+ * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags, eps), MXF_E_DEVICE, MXF_E_HIP.
+ * Timed under the profiling name norm_fwd. */
+mxf_status mxf_layer_norm_fwd(const mxf_norm_desc* desc /* host */, const void* x, const void* weight,
+                              const void* bias, void* y, float* mean, float* rstd, void* ckpt_q,
+                              void* ckpt_s, void* stream);
+
+/* Backward, from x with its mean and rstd, or (x and mean NULL) from the checkpoint and rstd: xh is then
+ * the decoded checkpoint, so the gradients are those of the rounded rows. dweight, dbias [cols] FP32,
+ * overwritten, either may be NULL; equal inputs give equal bits (no atomics). workspace:
+ * mxf_layer_norm_workspace_bytes, 4-byte aligned; not needed (NULL) when both are NULL. dx may be dy or
+ * x. With rows = 0 dweight and dbias become zero.
+ * Errors: as forward. Timed under the profiling name norm_bwd. */
+size_t mxf_layer_norm_workspace_bytes(const mxf_norm_desc* desc /* host */); /* 0 if invalid */
+mxf_status mxf_layer_norm_bwd(const mxf_norm_desc* desc /* host */, const void* dy, const void* x,
+                              const void* ckpt_q, const void* ckpt_s, const float* mean, const float* rstd,
+                              const void* weight, void* dx, float* dweight, float* dbias, void* workspace,
+                              void* stream);
+
+/* ------------------------------------------------------------------ SwiGLU with 8-bit checkpoints */
+
+/* Forward: gu [rows, 2F] BF16 with row stride ldgu (gate in columns [0, F), up in [F, 2F));
+ * h [rows, F] BF16 with row stride ldh = BF16(g sigmoid(g) u), from the unrounded g and u. What the
+ * backward needs of gu is kept in 8 bits: q [rows, 2, F] and s [rows, 2, ceil(F / 32)], dense, the
+ * row-wise MXFP8 of each gate row and each up row (mxfp8_dequantize reads them as 2 rows x F).
+ * F in [1, 2^20], strides >= their width; BF16 pointers 2-byte aligned (16-byte aligned rows are faster).
+ * rows = 0 is a no-op that accepts NULL pointers.
+ * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_DEVICE, MXF_E_HIP. Profiling name
+ * swiglu_ckpt_fwd. */
+mxf_status mxf_swiglu_ckpt_fwd(const void* gu, int64_t rows, int64_t F, int64_t ldgu, void* h, int64_t ldh,
+                               void* q, void* s, void* stream);
+
+/* Backward from the checkpoint (g, u decoded, sg = sigmoid(g)): dgu [rows, 2F] = BF16(dh u sg
+ * (1 + g (1 - sg))) | BF16(dh g sg), and, unless h is NULL, h [rows, F] = BF16(g sg u): the activation
+ * again, for the weight gradient of the product that consumed it. dh [rows, F] BF16, row stride lddh;
+ * row strides lddgu and ldh. Errors: as forward. Profiling name swiglu_ckpt_bwd. */
+mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, const void* s, int64_t rows,
+                               int64_t F, void* dgu, int64_t lddgu, void* h, int64_t ldh, void* stream);
+
+/* ------------------------------------------------------------------ ragged expert products */
+
+/* BF16 matrix products grouped by expert, without padding: expert e owns rows [offs[e], offs[e+1]) of
+ * x [M, K] and y [M, N], any count, none included, and the weight w[e] of w [E, N, K] (dense):
+ *   grouped_gemm_fwd    y[r, n] = sum_k x[r, k] w[e, n, k]
+ *   grouped_gemm_dgrad  dx[r, k] = sum_n dy[r, n] w[e, n, k]
+ *   grouped_gemm_wgrad  dw[e, n, k] = sum over e's rows r of dy[r, n] x[r, k]
+ * FP32 accumulation; outputs BF16, or FP32 with MXF_GROUPED_OUT_F32. offs: int32 [E+1] on the device,
+ * offs[0] = 0, non-decreasing, offs[E] <= M (mxf_route_plan with pad_multiple 1 writes them so). Rows
+ * at or past offs[E] are never read or written. An expert without rows gets a zero dw (or keeps it,
+ * accumulating). A violation of the contract makes the kernel write no output; *status (int32 on the
+ * device, may be NULL) becomes MXF_DEV_OK or MXF_DEV_BAD_OFFSETS.
+ * wgrad's x: BF16 x, or (x NULL) its row-wise MXFP8, x_q [M, K] and x_s [M, ceil(K / 32)], dense, as
+ * mxfp8_quantize writes them; the codes are decoded in the kernel.
+ * A product too small for its tiles (few rows per expert) is bound by the weights' bytes; fwd then
+ * streams each met expert's weight once.
+ * Limits: E in [1, 1024]; M in [0, 2^30]; N, K in [1, 2^20]; ldx >= K, ldy >= N. Pointers aligned to
+ * their elements, int32 arrays to 4; rows of 16-byte alignment (N, K, ldx, ldy multiples of 8; wgrad
+ * from codes: K a multiple of 32) take the fast kernels. Outputs may not overlap inputs.
+ * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags), MXF_E_DEVICE, MXF_E_HIP. Profiling
+ * names grouped_fwd, grouped_dgrad, grouped_wgrad. */
+#define MXF_GROUPED_OUT_F32 1u  /* y, dx or dw is FP32 instead of BF16 */
+#define MXF_GROUPED_ACCUM 2u    /* wgrad with MXF_GROUPED_OUT_F32: add to dw instead of overwriting it */
+
+typedef struct {
+  int32_t E;
+  uint32_t flags;
+  int64_t M;
+  int64_t N;
+  int64_t K;
+  int64_t ldx;  /* elements between rows of x and dx (wgrad from codes: not used) */
+  int64_t ldy;  /* elements between rows of y and dy */
+} mxf_grouped_desc;
+
+mxf_status grouped_gemm_fwd(const mxf_grouped_desc* desc /* host */, const int32_t* offs, const void* x,
+                            const void* w, void* y, int32_t* status, void* stream);
+mxf_status grouped_gemm_dgrad(const mxf_grouped_desc* desc /* host */, const int32_t* offs, const void* dy,
+                              const void* w, void* dx, int32_t* status, void* stream);
+mxf_status grouped_gemm_wgrad(const mxf_grouped_desc* desc /* host */, const int32_t* offs, const void* dy,
+                              const void* x, const void* x_q, const void* x_s, void* dw, int32_t* status,
+                              void* stream);
+
 /* Synchronises `stream` and copies the device status word of the last fwd/bwd call that
  * used `workspace` into *device_status (MXF_DEV_OK or MXF_DEV_BAD_OFFSETS). */
 mxf_status mxf_read_status(const void* workspace, void* stream, int32_t* device_status /* host */);
@@ -329,7 +438,8 @@ mxf_status mxf_read_status(const void* workspace, void* stream, int32_t* device_
  * fc2_dgrad_dswiglu, bwd_gemms (FC1 wgrad, FC2 wgrad and FC1 dgrad in one launch, on 256-row
  * tiles: pad_multiple 256, D and 2F multiples of 256, not with MXF_CONCURRENT; otherwise
  * fc2_wgrad, fc1_wgrad, fc1_dgrad) (MXF_UNFUSED: fc1, swiglu_quant, fc2_dgrad, dswiglu_quant),
- * quantize, dequantize, route_plan, permute, dispatch_quant_x, hbm_read, hbm_write, hbm_copy.
+ * quantize, dequantize, route_plan, permute, dispatch_quant_x, norm_fwd, norm_bwd, swiglu_ckpt_fwd,
+ * swiglu_ckpt_bwd, grouped_fwd, grouped_dgrad, grouped_wgrad, hbm_read, hbm_write, hbm_copy.
  * Errors: MXF_E_ARG (capacity < 1 or > 1<<20, or end without begin), MXF_E_NULL, MXF_E_HIP. */
 typedef struct {
   char name[32];

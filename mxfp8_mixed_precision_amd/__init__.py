@@ -12,7 +12,13 @@ from ._abi import (CAP_GFX950, COL, DEBUG_F32, DEQ_BF16, DEQ_E5M2, DEQ_F32, E5M2
                    last_error, lib, make_desc, mlp_saved_bytes, mlp_tensor, mlp_workspace_bytes,
                    mxfp8_quantize, pack_w13, profile_begin, profile_end, quantize, query_device,
                    read_status, unpack_w13, hbm_probe, HBM_READ, HBM_WRITE, HBM_COPY,
-                   mfma_probe, MFMA_MATRIX, MFMA_STAGE)
+                   mfma_probe, MFMA_MATRIX, MFMA_STAGE, NormDesc, GroupedDesc, NORM_F32, NORM_WEIGHT_F32,
+                   GROUPED_OUT_F32, GROUPED_ACCUM, layer_norm_workspace_bytes, mxf_layer_norm_fwd,
+                   mxf_layer_norm_bwd, mxf_swiglu_ckpt_fwd, mxf_swiglu_ckpt_bwd, mxf_grouped_gemm_fwd,
+                   mxf_grouped_gemm_dgrad, mxf_grouped_gemm_wgrad)
+from .block_ops import (grouped_gemm_dgrad, grouped_gemm_fwd, grouped_gemm_wgrad, layer_norm_bwd,
+                        layer_norm_ckpt_bwd, layer_norm_ckpt_fwd, layer_norm_fwd, swiglu_ckpt_bwd,
+                        swiglu_ckpt_fwd)
 
 # shapes of the documented tensors, as functions of (E, D, F, m_capacity)
 _SHAPES = {

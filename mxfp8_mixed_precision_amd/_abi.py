@@ -23,6 +23,8 @@ CAP_GFX950 = 1
 ROW, COL, E5M2 = 1, 2, 4
 OUT_F32, DEBUG_F32, SERIAL, UNFUSED, X_QUANTIZED, CONCURRENT = 1, 2, 4, 8, 16, 32
 DEQ_BF16, DEQ_F32, DEQ_E5M2 = 0, 1, 2
+NORM_F32, NORM_WEIGHT_F32 = 1, 2
+GROUPED_OUT_F32, GROUPED_ACCUM = 1, 2
 
 # tensor ids (mxf_tensor)
 TENSORS = ["STATUS", "XQ_R", "XS_R", "XQ_C", "XS_C", "W13Q_R", "W13S_R", "W13Q_C", "W13S_C",
@@ -36,7 +38,10 @@ EXPORTS = ["mxf_abi_version", "mxf_query_device", "mxf_last_error", "mxfp8_quant
            "grouped_mlp_bwd", "mxf_read_status", "mxf_profile_begin", "mxf_profile_end",
            "mxf_pack_w13", "mxf_unpack_w13", "mxf_route_plan_workspace_bytes", "mxf_route_plan", "mxf_route_plan_noalloc",
            "mxf_dispatch_permute",
-           "mxfp8_dispatch_quantize", "mxf_hbm_probe", "mxf_mfma_probe"]
+           "mxfp8_dispatch_quantize", "mxf_hbm_probe", "mxf_mfma_probe",
+           "mxf_layer_norm_fwd", "mxf_layer_norm_bwd", "mxf_layer_norm_workspace_bytes",
+           "mxf_swiglu_ckpt_fwd", "mxf_swiglu_ckpt_bwd",
+           "grouped_gemm_fwd", "grouped_gemm_dgrad", "grouped_gemm_wgrad"]
 
 
 class MxfError(RuntimeError):
@@ -53,6 +58,17 @@ class MlpDesc(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("D", ctypes.c_int32), ("F", ctypes.c_int32),
                 ("pad_multiple", ctypes.c_int32), ("m_capacity", ctypes.c_int64),
                 ("flags", ctypes.c_uint32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("lddx", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class GroupedDesc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("flags", ctypes.c_uint32), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 _lib = None
@@ -92,6 +108,15 @@ def lib():
             "mxfp8_dispatch_quantize": (ctypes.c_int, [pdesc, vp, vp, vp, vp, i64, i32, vp, vp, vp]),
             "mxf_hbm_probe": (ctypes.c_int, [i32, vp, vp, i64, vp]),
             "mxf_mfma_probe": (ctypes.c_int, [i32, vp, i64, i32, i32, vp, vp]),
+            "mxf_layer_norm_fwd": (ctypes.c_int, [ctypes.POINTER(NormDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "mxf_layer_norm_workspace_bytes": (sz, [ctypes.POINTER(NormDesc)]),
+            "mxf_layer_norm_bwd": (ctypes.c_int, [ctypes.POINTER(NormDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                  vp]),
+            "mxf_swiglu_ckpt_fwd": (ctypes.c_int, [vp, i64, i64, i64, vp, i64, vp, vp, vp]),
+            "mxf_swiglu_ckpt_bwd": (ctypes.c_int, [vp, i64, vp, vp, i64, i64, vp, i64, vp, i64, vp]),
+            "grouped_gemm_fwd": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp]),
+            "grouped_gemm_dgrad": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp]),
+            "grouped_gemm_wgrad": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -304,6 +329,52 @@ MFMA_MATRIX, MFMA_STAGE = 0, 1
 def mfma_probe(mode, src, nbytes, stages, blocks, out, stream=None):
     """Matrix-core ceiling kernel (see mxf_mfma_probe): mode MFMA_MATRIX or MFMA_STAGE."""
     _check(lib().mxf_mfma_probe(mode, _ptr(src), nbytes, stages, blocks, _ptr(out), _stream(stream)))
+
+
+def mxf_layer_norm_fwd(desc, x, weight, bias, y, mean, rstd, ckpt_q, ckpt_s, stream=None):
+    """Raw call: pointers (tensors or ints) and a NormDesc, as in the C header."""
+    _check(lib().mxf_layer_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
+                                    _ptr(rstd), _ptr(ckpt_q), _ptr(ckpt_s), _stream(stream)))
+
+
+def layer_norm_workspace_bytes(desc):
+    return lib().mxf_layer_norm_workspace_bytes(ctypes.byref(desc))
+
+
+def mxf_layer_norm_bwd(desc, dy, x, ckpt_q, ckpt_s, mean, rstd, weight, dx, dweight, dbias, workspace, stream=None):
+    """Raw call: pointers (tensors or ints) and a NormDesc, as in the C header."""
+    _check(lib().mxf_layer_norm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(ckpt_q), _ptr(ckpt_s), _ptr(mean),
+                                    _ptr(rstd), _ptr(weight), _ptr(dx), _ptr(dweight), _ptr(dbias),
+                                    _ptr(workspace), _stream(stream)))
+
+
+def mxf_swiglu_ckpt_fwd(gu, rows, F, ldgu, h, ldh, q, s, stream=None):
+    """Raw call: pointers (tensors or ints) and sizes, as in the C header."""
+    _check(lib().mxf_swiglu_ckpt_fwd(_ptr(gu), rows, F, ldgu, _ptr(h), ldh, _ptr(q), _ptr(s), _stream(stream)))
+
+
+def mxf_swiglu_ckpt_bwd(dh, lddh, q, s, rows, F, dgu, lddgu, h, ldh, stream=None):
+    """Raw call: pointers (tensors or ints) and sizes, as in the C header."""
+    _check(lib().mxf_swiglu_ckpt_bwd(_ptr(dh), lddh, _ptr(q), _ptr(s), rows, F, _ptr(dgu), lddgu, _ptr(h), ldh,
+                                     _stream(stream)))
+
+
+def mxf_grouped_gemm_fwd(desc, offs, x, w, y, status=None, stream=None):
+    """Raw call of grouped_gemm_fwd: pointers (tensors or ints) and a GroupedDesc, as in the C header."""
+    _check(lib().grouped_gemm_fwd(ctypes.byref(desc), _ptr(offs), _ptr(x), _ptr(w), _ptr(y), _ptr(status),
+                                  _stream(stream)))
+
+
+def mxf_grouped_gemm_dgrad(desc, offs, dy, w, dx, status=None, stream=None):
+    """Raw call of grouped_gemm_dgrad."""
+    _check(lib().grouped_gemm_dgrad(ctypes.byref(desc), _ptr(offs), _ptr(dy), _ptr(w), _ptr(dx), _ptr(status),
+                                    _stream(stream)))
+
+
+def mxf_grouped_gemm_wgrad(desc, offs, dy, x, x_q, x_s, dw, status=None, stream=None):
+    """Raw call of grouped_gemm_wgrad."""
+    _check(lib().grouped_gemm_wgrad(ctypes.byref(desc), _ptr(offs), _ptr(dy), _ptr(x), _ptr(x_q), _ptr(x_s),
+                                    _ptr(dw), _ptr(status), _stream(stream)))
 
 
 def profile_begin(capacity=4096):

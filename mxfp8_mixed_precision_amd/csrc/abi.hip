@@ -63,6 +63,20 @@ mxf_status check_device() {
   return MXF_OK;
 }
 
+// Compute units of the current device (after check_device; cached per device).
+std::atomic<int> g_dev_cus[kMaxDevices];
+mxf_status cu_count(int* n) {
+  int dev = 0;
+  MXF_HIP(hipGetDevice(&dev), "hipGetDevice");
+  int c = g_dev_cus[dev].load(std::memory_order_relaxed);
+  if (c == 0) {
+    MXF_HIP(hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev), "CU count");
+    g_dev_cus[dev].store(c, std::memory_order_relaxed);
+  }
+  *n = c;
+  return MXF_OK;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -661,6 +675,221 @@ mxf_status mxfp8_dispatch_quantize(const mxf_mlp_desc* desc, const int32_t* offs
                                            T(MXF_T_XQ_C), T(MXF_T_XS_C), (int32_t*)T(MXF_T_STATUS), st);
           }), "dispatch quantize launch");
   return MXF_OK;
+}
+
+// ------------------------------------------------------------------ layer norm
+
+static bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+static mxf_status check_norm_desc(const mxf_norm_desc* d, bool bwd) {
+  if (!d) return fail(MXF_E_NULL, "desc is NULL");
+  if (d->rows < 0 || d->rows > ((int64_t)1 << 40))
+    return fail(MXF_E_SHAPE, "rows = %lld: must be in [0, 2^40]", (long long)d->rows);
+  if (d->cols < 1 || d->cols > (1 << 20))
+    return fail(MXF_E_SHAPE, "cols = %lld: must be in [1, 2^20]", (long long)d->cols);
+  if (d->ldx < d->cols || d->ldy < d->cols || (bwd && d->lddx < d->cols))
+    return fail(MXF_E_SHAPE, "ldx = %lld, ldy = %lld, lddx = %lld: must be at least cols (%lld)", (long long)d->ldx,
+                (long long)d->ldy, (long long)d->lddx, (long long)d->cols);
+  if (!(d->eps >= 0.0f)) return fail(MXF_E_ARG, "eps = %g: must not be negative", (double)d->eps);
+  if (d->flags & ~(uint32_t)(MXF_NORM_F32 | MXF_NORM_WEIGHT_F32))
+    return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
+  return MXF_OK;
+}
+
+mxf_status mxf_layer_norm_fwd(const mxf_norm_desc* desc, const void* x, const void* weight, const void* bias, void* y,
+                              float* mean, float* rstd, void* ckpt_q, void* ckpt_s, void* stream) {
+  g_err.clear();
+  mxf_status s = check_norm_desc(desc, false);
+  if (s != MXF_OK) return s;
+  if (desc->rows == 0) return MXF_OK;
+  if (!x || !y) return fail(MXF_E_NULL, "x or y is NULL");
+  if (!ckpt_q != !ckpt_s) return fail(MXF_E_NULL, "one of ckpt_q and ckpt_s is NULL");
+  const size_t esz = desc->flags & MXF_NORM_F32 ? 4 : 2, wsz = desc->flags & MXF_NORM_WEIGHT_F32 ? 4 : 2;
+  if (!aligned_to(x, esz) || !aligned_to(y, esz)) return fail(MXF_E_ALIGN, "x or y is not aligned to its elements");
+  if (!aligned_to(weight, wsz) || !aligned_to(bias, wsz))
+    return fail(MXF_E_ALIGN, "weight or bias is not aligned to its elements");
+  if (!aligned4(mean) || !aligned4(rstd)) return fail(MXF_E_ALIGN, "mean or rstd is not 4-byte aligned");
+  if ((s = check_device()) != MXF_OK) return s;
+  mxf::NormParams p = {};
+  p.x = x; p.w = weight; p.b = bias; p.y = y; p.mean = mean; p.rstd = rstd;
+  p.q = (uint8_t*)ckpt_q; p.s = (uint8_t*)ckpt_s;
+  p.rows = desc->rows; p.cols = desc->cols; p.ldx = desc->ldx; p.ldy = desc->ldy;
+  p.eps = desc->eps;
+  p.w_f32 = wsz == 4;
+  MXF_HIP(timed("norm_fwd", (hipStream_t)stream, [&] { return mxf_launch_norm_fwd(p, esz == 4, (hipStream_t)stream); }),
+          "layer norm forward launch");
+  return MXF_OK;
+}
+
+size_t mxf_layer_norm_workspace_bytes(const mxf_norm_desc* desc) {
+  g_err.clear();
+  if (check_norm_desc(desc, false) != MXF_OK) return 0;
+  const int parts = mxf_norm_parts(desc->rows, desc->cols);
+  return (size_t)(parts > 0 ? parts : 1) * 2 * (size_t)desc->cols * sizeof(float);
+}
+
+mxf_status mxf_layer_norm_bwd(const mxf_norm_desc* desc, const void* dy, const void* x, const void* ckpt_q,
+                              const void* ckpt_s, const float* mean, const float* rstd, const void* weight, void* dx,
+                              float* dweight, float* dbias, void* workspace, void* stream) {
+  g_err.clear();
+  mxf_status s = check_norm_desc(desc, true);
+  if (s != MXF_OK) return s;
+  if ((dweight || dbias) && !workspace) return fail(MXF_E_NULL, "workspace is NULL");
+  if (!aligned4(dweight) || !aligned4(dbias) || !aligned4(workspace))
+    return fail(MXF_E_ALIGN, "dweight, dbias or workspace is not 4-byte aligned");
+  const size_t esz = desc->flags & MXF_NORM_F32 ? 4 : 2, wsz = desc->flags & MXF_NORM_WEIGHT_F32 ? 4 : 2;
+  if (desc->rows > 0) {
+    if (!dy || !dx || !rstd) return fail(MXF_E_NULL, "dy, dx or rstd is NULL");
+    if (!ckpt_q != !ckpt_s) return fail(MXF_E_NULL, "one of ckpt_q and ckpt_s is NULL");
+    if (ckpt_q && x) return fail(MXF_E_ARG, "both x and a checkpoint given");
+    if (!ckpt_q && (!x || !mean)) return fail(MXF_E_NULL, "x or mean is NULL without a checkpoint");
+    if (!aligned_to(dy, esz) || !aligned_to(x, esz) || !aligned_to(dx, esz))
+      return fail(MXF_E_ALIGN, "dy, x or dx is not aligned to its elements");
+    if (!aligned_to(weight, wsz)) return fail(MXF_E_ALIGN, "weight is not aligned to its elements");
+    if (!aligned4(mean) || !aligned4(rstd)) return fail(MXF_E_ALIGN, "mean or rstd is not 4-byte aligned");
+  } else if (!dweight && !dbias) {
+    return MXF_OK;
+  }
+  if ((s = check_device()) != MXF_OK) return s;
+  mxf::NormParams p = {};
+  p.dy = dy; p.w = weight; p.dx = dx;
+  p.x = ckpt_q ? nullptr : x;
+  p.q = (uint8_t*)const_cast<void*>(ckpt_q);
+  p.s = (uint8_t*)const_cast<void*>(ckpt_s);
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.part = dweight || dbias ? (float*)workspace : nullptr;
+  p.dw = dweight;
+  p.db = dbias;
+  p.rows = desc->rows; p.cols = desc->cols; p.ldx = desc->ldx; p.ldy = desc->ldy; p.lddx = desc->lddx;
+  p.w_f32 = wsz == 4;
+  MXF_HIP(timed("norm_bwd", (hipStream_t)stream, [&] { return mxf_launch_norm_bwd(p, esz == 4, (hipStream_t)stream); }),
+          "layer norm backward launch");
+  return MXF_OK;
+}
+
+// ------------------------------------------------------------------ SwiGLU with 8-bit checkpoints
+
+static mxf_status check_swiglu(int64_t rows, int64_t F, int64_t ldgu, int64_t ldh) {
+  if (rows < 0 || rows > ((int64_t)1 << 40)) return fail(MXF_E_SHAPE, "rows = %lld: must be in [0, 2^40]", (long long)rows);
+  if (F < 1 || F > (1 << 20)) return fail(MXF_E_SHAPE, "F = %lld: must be in [1, 2^20]", (long long)F);
+  if (ldgu < 2 * F) return fail(MXF_E_SHAPE, "row stride %lld of gate and up: must be at least 2F (%lld)",
+                                (long long)ldgu, (long long)(2 * F));
+  if (ldh < F) return fail(MXF_E_SHAPE, "row stride %lld of h or dh: must be at least F (%lld)", (long long)ldh,
+                           (long long)F);
+  return MXF_OK;
+}
+
+mxf_status mxf_swiglu_ckpt_fwd(const void* gu, int64_t rows, int64_t F, int64_t ldgu, void* h, int64_t ldh, void* q,
+                               void* s, void* stream) {
+  g_err.clear();
+  mxf_status st = check_swiglu(rows, F, ldgu, ldh);
+  if (st != MXF_OK) return st;
+  if (rows == 0) return MXF_OK;
+  if (!gu || !h || !q || !s) return fail(MXF_E_NULL, "gu, h, q or s is NULL");
+  if (!aligned_to(gu, 2) || !aligned_to(h, 2)) return fail(MXF_E_ALIGN, "gu or h is not 2-byte aligned");
+  if ((st = check_device()) != MXF_OK) return st;
+  MXF_HIP(timed("swiglu_ckpt_fwd", (hipStream_t)stream, [&] {
+            return mxf_launch_swiglu_ckpt_fwd(gu, rows, F, ldgu, ldh, h, q, s, (hipStream_t)stream);
+          }), "SwiGLU forward launch");
+  return MXF_OK;
+}
+
+mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, const void* s, int64_t rows, int64_t F,
+                               void* dgu, int64_t lddgu, void* h, int64_t ldh, void* stream) {
+  g_err.clear();
+  mxf_status st = check_swiglu(rows, F, lddgu, lddh);
+  if (st != MXF_OK) return st;
+  if (h && ldh < F) return fail(MXF_E_SHAPE, "ldh = %lld: must be at least F (%lld)", (long long)ldh, (long long)F);
+  if (rows == 0) return MXF_OK;
+  if (!dh || !q || !s || !dgu) return fail(MXF_E_NULL, "dh, q, s or dgu is NULL");
+  if (!aligned_to(dh, 2) || !aligned_to(dgu, 2) || !aligned_to(h, 2))
+    return fail(MXF_E_ALIGN, "dh, dgu or h is not 2-byte aligned");
+  if ((st = check_device()) != MXF_OK) return st;
+  MXF_HIP(timed("swiglu_ckpt_bwd", (hipStream_t)stream, [&] {
+            return mxf_launch_swiglu_ckpt_bwd(dh, q, s, rows, F, lddh, lddgu, ldh, dgu, h, (hipStream_t)stream);
+          }), "SwiGLU backward launch");
+  return MXF_OK;
+}
+
+// ------------------------------------------------------------------ ragged expert products
+
+static mxf_status check_grouped_desc(const mxf_grouped_desc* d, bool wgrad) {
+  if (!d) return fail(MXF_E_NULL, "desc is NULL");
+  if (d->E < 1 || d->E > 1024) return fail(MXF_E_SHAPE, "E = %d: must be in [1, 1024]", d->E);
+  if (d->M < 0 || d->M > ((int64_t)1 << 30)) return fail(MXF_E_SHAPE, "M = %lld: must be in [0, 2^30]", (long long)d->M);
+  if (d->N < 1 || d->N > (1 << 20) || d->K < 1 || d->K > (1 << 20))
+    return fail(MXF_E_SHAPE, "N = %lld, K = %lld: must be in [1, 2^20]", (long long)d->N, (long long)d->K);
+  if (d->ldx < d->K || d->ldy < d->N)
+    return fail(MXF_E_SHAPE, "ldx = %lld, ldy = %lld: must be at least K (%lld) and N (%lld)", (long long)d->ldx,
+                (long long)d->ldy, (long long)d->K, (long long)d->N);
+  if (d->flags & ~(uint32_t)(MXF_GROUPED_OUT_F32 | MXF_GROUPED_ACCUM))
+    return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
+  if ((d->flags & MXF_GROUPED_ACCUM) && (!wgrad || !(d->flags & MXF_GROUPED_OUT_F32)))
+    return fail(MXF_E_ARG, "flags = 0x%x: MXF_GROUPED_ACCUM is for wgrad with MXF_GROUPED_OUT_F32", d->flags);
+  return MXF_OK;
+}
+
+// `left`, `right`: BF16 operands (right may be null where codes are given), `out`: the result.
+static mxf_status run_grouped(int op, const char* name, const mxf_grouped_desc* d, const int32_t* offs,
+                              const void* left, const void* right, const void* rq, const void* rs, void* out,
+                              int32_t* status, void* stream) {
+  mxf_status s = check_grouped_desc(d, op == 2);
+  if (s != MXF_OK) return s;
+  if (!offs) return fail(MXF_E_NULL, "offs is NULL");
+  if (!aligned4(offs) || !aligned4(status)) return fail(MXF_E_ALIGN, "offs or status is not 4-byte aligned");
+  const bool rows = d->M > 0;  // without rows the row operands may be NULL
+  if (rows && !left) return fail(MXF_E_NULL, op == 0 ? "x is NULL" : "dy is NULL");
+  if (op != 2 && rows && !right) return fail(MXF_E_NULL, "w is NULL");
+  if (op == 2 && rows && !right && (!rq || !rs)) return fail(MXF_E_NULL, "x is NULL, and so is x_q or x_s");
+  if (op == 2 && right && (rq || rs)) return fail(MXF_E_ARG, "both x and its codes given");
+  if ((op == 2 || rows) && !out) return fail(MXF_E_NULL, op == 0 ? "y is NULL" : op == 1 ? "dx is NULL" : "dw is NULL");
+  const bool f32 = (d->flags & MXF_GROUPED_OUT_F32) != 0;
+  if (!aligned_to(left, 2) || !aligned_to(right, 2)) return fail(MXF_E_ALIGN, "an operand is not 2-byte aligned");
+  if (!aligned_to(out, f32 ? 4 : 2)) return fail(MXF_E_ALIGN, "the output is not aligned to its elements");
+  const int64_t ct = ((op == 0 ? d->N : d->K) + 127) / 128;
+  const int64_t rt = op == 2 ? d->E * ((d->N + 127) / 128) : d->M / 128 + d->E;
+  if (rt > 0xFFFFFF / ct)
+    return fail(MXF_E_SHAPE, "E = %d, M = %lld, N = %lld, K = %lld: more than 2^24 tiles", d->E, (long long)d->M,
+                (long long)d->N, (long long)d->K);
+  if ((s = check_device()) != MXF_OK) return s;
+  int ncu = 0;
+  if ((s = cu_count(&ncu)) != MXF_OK) return s;
+  mxf::GroupedParams p = {};
+  p.a = (const uint16_t*)left;
+  p.b = (const uint16_t*)right;
+  p.bq = op == 2 && !right ? (const uint8_t*)rq : nullptr;
+  p.bs = (const uint8_t*)rs;
+  p.c = out;
+  p.offs = offs;
+  p.status = status;
+  p.M = d->M; p.N = d->N; p.K = d->K; p.E = d->E;
+  p.lda = op == 0 ? d->ldx : d->ldy;
+  p.ldb = op == 2 ? d->ldx : d->K;
+  p.ldc = op == 0 ? d->ldy : op == 1 ? d->ldx : d->K;
+  p.out_f32 = f32;
+  p.accum = (d->flags & MXF_GROUPED_ACCUM) != 0;
+  MXF_HIP(timed(name, (hipStream_t)stream, [&] { return mxf_launch_grouped(op, p, ncu, (hipStream_t)stream); }),
+          "grouped product launch");
+  return MXF_OK;
+}
+
+mxf_status grouped_gemm_fwd(const mxf_grouped_desc* desc, const int32_t* offs, const void* x, const void* w, void* y,
+                            int32_t* status, void* stream) {
+  g_err.clear();
+  return run_grouped(0, "grouped_fwd", desc, offs, x, w, nullptr, nullptr, y, status, stream);
+}
+
+mxf_status grouped_gemm_dgrad(const mxf_grouped_desc* desc, const int32_t* offs, const void* dy, const void* w,
+                              void* dx, int32_t* status, void* stream) {
+  g_err.clear();
+  return run_grouped(1, "grouped_dgrad", desc, offs, dy, w, nullptr, nullptr, dx, status, stream);
+}
+
+mxf_status grouped_gemm_wgrad(const mxf_grouped_desc* desc, const int32_t* offs, const void* dy, const void* x,
+                              const void* x_q, const void* x_s, void* dw, int32_t* status, void* stream) {
+  g_err.clear();
+  return run_grouped(2, "grouped_wgrad", desc, offs, dy, x, x_q, x_s, dw, status, stream);
 }
 
 mxf_status mxf_read_status(const void* workspace, void* stream, int32_t* device_status) {

@@ -41,8 +41,57 @@ struct GemmParams {
   float* dbg;        // optional fp32 copy of the accumulator ([mcap, N])
 };
 
+// Layer norm (norm.hip). Element type (BF16 or FP32) of x, y, dy and dx is a launch argument;
+// strides in elements. A null w is 1, a null b is 0.
+struct NormParams {
+  const void* x;      // forward, and backward without a checkpoint
+  const void* dy;
+  const void* w;
+  const void* b;
+  void* y;
+  void* dx;
+  float* mean;        // forward: written unless null; backward: read unless the checkpoint is
+  float* rstd;
+  uint8_t* q;         // checkpoint codes [rows, cols] (null: none) and scales [rows, ceil(cols / 32)]
+  uint8_t* s;
+  float* part;        // backward workspace: [parts][dw, db][cols]; null: dw and db are not wanted
+  float* dw;
+  float* db;
+  int64_t rows, cols, ldx, ldy, lddx;
+  float eps;
+  bool w_f32;
+};
+
+// Expert products over ragged row segments (grouped.hip). OP 0: y = x w^T, 1: dx = dy w,
+// 2: dw = dy^T x. a, b: the left and right operand; contraction over `kc`; output [om, on] (per expert
+// for OP 2). Strides in elements.
+struct GroupedParams {
+  const uint16_t* a;  // OP 0: x [M, K], 1: dy [M, N], 2: dy [M, N]
+  const uint16_t* b;  // OP 0, 1: w [E, N, K], 2: x [M, K] (null: codes)
+  const uint8_t* bq;  // OP 2: codes of x [M, K] and scales [M, ceil(K / 32)]
+  const uint8_t* bs;
+  void* c;
+  const int32_t* offs;
+  int32_t* status;    // may be null
+  int64_t M, N, K;
+  int64_t lda, ldb, ldc;
+  int E;
+  int out_f32, accum;
+};
+
 }  // namespace mxf
 
+// norm.hip
+int mxf_norm_parts(int64_t rows, int64_t cols);
+hipError_t mxf_launch_norm_fwd(const mxf::NormParams& p, bool f32, hipStream_t st);
+hipError_t mxf_launch_norm_bwd(const mxf::NormParams& p, bool f32, hipStream_t st);
+// swiglu_ckpt.hip
+hipError_t mxf_launch_swiglu_ckpt_fwd(const void* gu, int64_t rows, int64_t F, int64_t ldgu, int64_t ldh, void* h,
+                                      void* q, void* s, hipStream_t st);
+hipError_t mxf_launch_swiglu_ckpt_bwd(const void* dh, const void* q, const void* s, int64_t rows, int64_t F,
+                                      int64_t lddh, int64_t lddgu, int64_t ldh, void* dgu, void* h, hipStream_t st);
+// grouped.hip
+hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipStream_t st);
 // quantize.hip
 hipError_t mxf_launch_quantize(const void* x, int64_t rows, int64_t cols, uint32_t mode, bool e5m2, void* q_row,
                                void* s_row, void* q_col, void* s_col, hipStream_t st);
