@@ -118,24 +118,11 @@ struct Tile {
 // 16 distinct 16-byte bank groups.
 __device__ __forceinline__ int swz(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4); }
 
-// s_waitcnt with only the vector-memory counter constrained (gfx9 encoding: vmcnt low bits
-// [3:0] and high bits [15:14]; expcnt 7 and lgkmcnt 15 mean "no wait").
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt out of range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
 // Direct global -> LDS loads (gfx950 global_load_lds_dword{,x4}): lane l's bytes land at LDS
 // address m0 + size * l. Written as inline asm so that the compiler's wait insertion does not
 // treat every LDS read as aliasing the in-flight fills (it would drain the pipeline with
 // vmcnt(0) before each read); the kernel waits on vmcnt itself. M0 is set in the same asm
 // block and clobbered; the instruction has no destination VGPRs.
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(lds_ptr)p;
-}
 // Address = wavefront-uniform 64-bit base (SGPRs) + per-lane 32-bit offset (one VGPR).
 __device__ __forceinline__ void g2lds4(const void* sbase, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(sbase) : "memory", "m0");
@@ -156,14 +143,6 @@ __device__ __forceinline__ void g2lds16_q(int q, const void* sbase, uint32_t vof
     default: g2lds16_off<3072>(sbase, voff, lds); break;
   }
 }
-
-// LDS reads through a 32-bit LDS byte address; constant offsets added to the returned pointer
-// fold into the instruction's offset field.
-typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) const u32x4_t lds_u4;
-typedef __attribute__((address_space(3))) const uint8_t lds_u8;
-__device__ __forceinline__ lds_u4* lds16_at(uint32_t a) { return (lds_u4*)(uintptr_t)a; }
-__device__ __forceinline__ lds_u8* lds8_at(uint32_t a) { return (lds_u8*)(uintptr_t)a; }
 
 // One output tile (rows [m0, m0 + BM), columns [n0, n0 + BN), contraction over [kbeg, kend)):
 // the pipelined main loop and the epilogue. smem holds Tile<BM, BN, WM, WN>::lds(EPI) bytes.

@@ -8,6 +8,8 @@
 // BF16 operands, FP32 accumulation in the matrix cores, one rounding at the store. A code of the
 // MXFP8 checkpoint has four significant bits, so its product with the scale is a BF16 number and
 // enters the same matrix instruction unrounded.
+#include <type_traits>
+
 #include "kernels.h"
 #include "mx_device.h"
 
@@ -16,47 +18,58 @@ namespace mxf {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// The contract of offs (offs[0] = 0, non-decreasing, offs[E] <= M) and, for a row tile index t, the
-// expert and rows that it covers; whole wavefronts, the same answer in every lane. Lane i looks at
-// expert 64 j + i; tiles are counted in expert order.
+// The contract of offs (offs[0] = 0, non-decreasing, offs[E] <= M), the number of row tiles of all
+// experts, and the expert and rows of row tile t. Whole wavefronts, the same answer in every lane:
+// lane i looks at expert 64 j + i, tiles are counted in expert order. Offsets that break the contract may
+// leave any counts behind; the caller stops on ok = false before it uses them.
 struct RowTile {
-  bool ok;        // offsets hold
-  int64_t tiles;  // row tiles of all experts
-  int e;          // -1: t is past the last tile
-  int64_t m0, m1; // rows of the tile
+  int e;       // -1: past the last tile
+  int m0, m1;  // rows of the tile
 };
-__device__ __forceinline__ RowTile find_row_tile(const int32_t* offs, int E, int64_t M, int bm, int64_t t) {
-  const int lane = threadIdx.x & 63;
-  RowTile r = {true, 0, -1, 0, 0};
+struct RowTiles {
+  bool ok;
+  int tiles;
+  int lo, hi, first, n;  // of the lane's last expert looked at (E <= 64: its only one)
+};
+__device__ __forceinline__ void scan_experts(const int32_t* offs, int E, int bm, int base, RowTiles& r) {
+  const int lane = threadIdx.x & 63, i = base + lane;
+  r.lo = i < E ? offs[i] : 0;
+  r.hi = i < E ? offs[i + 1] : 0;
+  r.n = r.hi > r.lo ? (int)(((uint32_t)r.hi - (uint32_t)r.lo + bm - 1) / bm) : 0;
+  int pre = r.n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(pre, o);
+    if (lane >= o) pre += v;
+  }
+  r.first = r.tiles + pre - r.n;
+  r.tiles += __builtin_amdgcn_readlane(pre, 63);
+}
+__device__ __forceinline__ RowTiles count_row_tiles(const int32_t* offs, int E, int64_t M, int bm) {
+  RowTiles r = {true, 0, 0, 0, 0, 0};
   bool bad = false;
   for (int base = 0; base < E; base += 64) {
-    const int i = base + lane;
-    const int32_t lo = i < E ? offs[i] : 0, hi = i < E ? offs[i + 1] : 0;
-    if (i < E && (lo > hi || lo < 0 || hi > M || (i == 0 && lo != 0))) bad = true;
-    const int32_t n = i < E && hi > lo ? (hi - lo + bm - 1) / bm : 0;
-    int32_t pre = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int32_t v = __shfl_up(pre, o);
-      if (lane >= o) pre += v;
-    }
-    const int64_t first = r.tiles + pre - n;
-    const uint64_t hit = __ballot(n > 0 && t >= first && t < first + n);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int32_t k = (int32_t)(t - __shfl(first, l));
-      const int32_t elo = __shfl(lo, l), ehi = __shfl(hi, l);
-      r.e = base + l;
-      r.m0 = (int64_t)elo + (int64_t)k * bm;
-      r.m1 = r.m0 + bm < ehi ? r.m0 + bm : ehi;
-    }
-    r.tiles += __shfl(pre, 63);
+    scan_experts(offs, E, bm, base, r);
+    bad = bad || r.lo > r.hi || r.lo < 0 || r.hi > M || (base == 0 && (threadIdx.x & 63) == 0 && r.lo != 0);
   }
   r.ok = !__any(bad);
   return r;
 }
+__device__ __forceinline__ RowTile find_row_tile(RowTiles r, const int32_t* offs, int E, int bm, int t) {
+  if (E > 64) r.tiles = 0;
+  for (int base = 0; base < E; base += 64) {
+    if (E > 64) scan_experts(offs, E, bm, base, r);
+    const uint64_t hit = __ballot(r.n > 0 && t >= r.first && t < r.first + r.n);
+    if (hit) {
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+      const int m0 = __builtin_amdgcn_readlane(r.lo, l) + (t - __builtin_amdgcn_readlane(r.first, l)) * bm;
+      return {base + l, m0, min(m0 + bm, __builtin_amdgcn_readlane(r.hi, l))};
+    }
+  }
+  return {-1, 0, 0};
+}
 
-// The same contract without a tile.
+// The contract alone.
 __device__ __forceinline__ bool ragged_ok(const int32_t* offs, int E, int64_t M) {
   bool bad = false;
   for (int i = threadIdx.x & 63; i < E; i += 64) {
@@ -94,9 +107,11 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedParams p, int64
     c0 = p.offs[e];
     c1 = p.offs[e + 1];
   } else {
-    const RowTile r = find_row_tile(p.offs, p.E, p.M, AT, blockIdx.x / col_tiles);
-    if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = r.ok ? 0 : 1;
-    if (!r.ok || r.e < 0) return;
+    const RowTiles rt = count_row_tiles(p.offs, p.E, p.M, AT);
+    if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = rt.ok ? 0 : 1;
+    if (!rt.ok) return;
+    const RowTile r = find_row_tile(rt, p.offs, p.E, AT, (int)(blockIdx.x / col_tiles));
+    if (r.e < 0) return;
     e = r.e;
     m0 = r.m0;
     m1 = r.m1;
@@ -171,18 +186,404 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedParams p, int64
       }
 }
 
+// ------------------------------------------------------------------ aligned rows: pipelined tiles
+
+// Block tile BM x BN, four wavefronts in a 2 x 2 grid, each owning a (BM/2) x (BN/2) tile of 32 x 32
+// matrix-core fragments (256 x 256: all 256 accumulators of a lane in AGPRs, one block per CU).
+//
+// The contraction advances 64 at a time through two LDS slots filled by direct global->LDS loads of
+// 1 KB. In a stage the 16-deep matrix instructions of one quarter run beside the LDS reads of the
+// next quarter; before the last quarter one wait and one barrier make the next stage visible and this
+// stage's slot free, and the last quarter issues the loads of the stage after the next into it.
+//
+// An operand is stored in LDS as it lies in memory:
+//   contraction-contiguous (x and dy of OP 0, 1; w of OP 0): rows of 64 elements (128 bytes), fragments
+//     read with ds_read_b128. 16-byte chunk c of row r sits at c ^ ((r / 2) % 8): 16 consecutive rows
+//     at one chunk index then hit 16 different 16-byte bank groups.
+//   contraction-slow (w of OP 1, both of OP 2): rows of BM or BN elements, one per contraction index,
+//     fragments read with the transposing ds_read_b64_tr_b16, which gives each of 16 lanes one
+//     column of four rows. Chunk c of row k sits at c ^ 4 (k % 4): the four rows of a read, 32 bytes
+//     each, and the two 16-column halves of a fragment hit eight different 32-byte bank groups.
+//
+// Bounds: the loads are buffer loads against a descriptor that ends at 2 GB from the tile's first
+// element; a lane whose row or column does not exist asks for an offset past it and gets zeros in
+// LDS. So ragged segment ends, odd tile ends and the last contraction stage need no other path, rows of
+// another expert are never read, and 64-bit offsets live in the descriptor's base.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr uint32_t kNoElement = 0x80000000u;  // = the descriptors' size
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+         ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+}
+// 16 bytes per lane into LDS [lds, lds + 1024) in lane order. The loads have no destination registers;
+// the kernel waits for them with vmcnt. (One wait state between a write of M0 and its use.)
+__device__ __forceinline__ void buffer_to_lds(i32x4 rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+__device__ __forceinline__ i32x4 descriptor(uint64_t base) {
+  return (i32x4){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xFFFFu), (int)kNoElement, 0x00020000};
+}
+
+// One operand of a tile: R rows or columns of the output, contraction-contiguous (KC) or not.
+template <bool KC, int R>
+struct Operand {
+  static constexpr int NLOAD = R / 32;         // 1 KB loads per wavefront and stage
+  static constexpr int CPR = R / 8;            // contraction-slow: 16-byte chunks per row
+  static constexpr int RPL = 64 / CPR;         // and rows per load
+  static constexpr int NR = KC ? 1 : 2;        // LDS reads per fragment
+  uint64_t base;      // first element of the stage to load next
+  uint64_t step;      // bytes between stages
+  uint32_t voff[NLOAD];
+  uint32_t k_lane;    // contraction index of the lane's first element: KC: of even loads, else of load 0
+  uint32_t rd[4];     // LDS read addresses in slot 0: KC: per quarter, else per fragment
+
+  // origin: the tile's first element; ld: elements between rows; `valid`: rows or columns that exist; w0:
+  // this wavefront's first row or column; lds: the operand's place in slot 0
+  __device__ __forceinline__ void init(const uint16_t* origin, int64_t ld, int valid, int wid, int w0, uint32_t lds) {
+    const int l = threadIdx.x & 63;
+    base = uniform64((uint64_t)origin);
+    step = KC ? 128 : (uint64_t)ld * 128;
+    const uint32_t ldb = (uint32_t)ld * 2;
+#pragma unroll
+    for (int i = 0; i < NLOAD; ++i) {
+      const int q = wid * NLOAD + i;
+      if constexpr (KC) {
+        const int r = 8 * q + (l >> 3), c = (l & 7) ^ ((r >> 1) & 7);
+        voff[i] = r < valid ? (uint32_t)r * ldb + c * 16 : kNoElement;
+      } else {
+        const int k = RPL * q + l / CPR, c = (l % CPR) ^ (4 * (k & 3));
+        voff[i] = c * 8 < valid ? (uint32_t)k * ldb + c * 16 : kNoElement;
+      }
+    }
+    k_lane = KC ? ((l & 7) ^ ((l >> 4) & 7)) * 8 : RPL * NLOAD * wid + l / CPR;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (KC) {
+        const int r = w0 + (l & 31), c = (2 * j + (l >> 5)) ^ ((r >> 1) & 7);
+        rd[j] = lds + r * 128 + c * 16;
+      } else {
+        const int k = 8 * (l >> 5) + ((l & 15) >> 2), c32 = (w0 >> 4) + 2 * j + ((l >> 4) & 1);
+        rd[j] = lds + k * (R * 2) + ((c32 ^ (2 * (k & 3))) << 5) + (l & 3) * 8;
+      }
+    }
+  }
+  // Load i of the stage at `base`, of which `left` contraction indexes exist, into LDS.
+  __device__ __forceinline__ void load(int i, int left, uint32_t lds) const {
+    // odd loads of a contraction-contiguous operand start four rows further, which flips chunk bit 2
+    const int k = KC ? (int)(k_lane ^ (32 * (i & 1))) : (int)k_lane + RPL * i;
+    buffer_to_lds(descriptor(base), k < left ? voff[i] : kNoElement, lds + i * 1024);
+  }
+  // Part h of fragment i in quarter s.
+  __device__ __forceinline__ void read(u32x4_t& f, int i, int h, int s, uint32_t slot) const {
+    if constexpr (KC) {
+      f = lds16_at(rd[s] + slot)[i * 256];
+    } else {
+      const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(uintptr_t)(rd[i] + slot + (16 * s + 4 * h) * (R * 2)));
+      const uint2 u = __builtin_bit_cast(uint2, v);
+      f[2 * h] = u.x;
+      f[2 * h + 1] = u.y;
+    }
+  }
+};
+
+template <int BM, int BN>
+struct TileSize {
+  static constexpr int FM = BM / 64, FN = BN / 64;
+  static constexpr int B_OFF = BM * 128;         // of a slot
+  static constexpr int SLOT = (BM + BN) * 128;
+  static constexpr int PITCH16 = BN + 8, PITCH32 = BN + 4;  // epilogue staging rows (elements)
+  static constexpr int EPI16 = BM * PITCH16 * 2, EPI32 = BM / 2 * PITCH32 * 4;
+  static constexpr int max3(int a, int b, int c) { return a > b ? (a > c ? a : c) : (b > c ? b : c); }
+  static constexpr int LDS = max3(2 * SLOT, EPI16, EPI32);
+};
+
+// Output rows [m0, m0 + mr) and columns [n0, n0 + nc) of the tile, contraction length kc; a and b: the
+// operands' first elements of the tile.
+template <int OP, int BM, int BN, bool F32>
+__device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* smem, const uint16_t* a, const uint16_t* b,
+                                             int64_t ldb, int64_t c_base, int mr, int nc, int kc) {
+  using S = TileSize<BM, BN>;
+  constexpr int FM = S::FM, FN = S::FN;
+  using OA = Operand<OP != 2, BM>;
+  using OB = Operand<OP == 0, BN>;
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+  const int wid_u = __builtin_amdgcn_readfirstlane(wid);
+  const int wm = wid >> 1, wn = wid & 1;
+  const uint32_t lds0 = lds_addr(smem);
+  OA oa;
+  OB ob;
+  oa.init(a, p.lda, mr, wid, wm * (BM / 2), lds0);
+  ob.init(b, ldb, nc, wid, wn * (BN / 2), lds0 + S::B_OFF);
+  const uint32_t lds_a = lds0 + wid_u * OA::NLOAD * 1024, lds_b = lds0 + S::B_OFF + wid_u * OB::NLOAD * 1024;
+  const int KT = (kc + 63) >> 6;
+
+  constexpr int NL = OA::NLOAD + OB::NLOAD;
+  auto issue = [&](int i, int ks) {  // load i of stage ks, whose first elements oa.base and ob.base point at
+    const int left = kc - ks * 64;
+    const uint32_t slot = (uint32_t)(ks & 1) * S::SLOT;
+    if (i < OA::NLOAD)
+      oa.load(i, left, lds_a + slot);
+    else
+      ob.load(i - OA::NLOAD, left, lds_b + slot);
+  };
+  auto advance = [&]() {
+    oa.base += oa.step;
+    ob.base += ob.step;
+  };
+
+  f32x16 acc[FM][FN];
+  u32x4_t fa[2][FM], fb[2][FN];
+  constexpr int NRA = FM * OA::NR, NR = NRA + FN * OB::NR;  // LDS reads of a quarter
+  auto read = [&](int r, int s, int set, uint32_t slot) {
+    if (r < NRA)
+      oa.read(fa[set][r / OA::NR], r / OA::NR, r % OA::NR, s, slot);
+    else
+      ob.read(fb[set][(r - NRA) / OB::NR], (r - NRA) / OB::NR, (r - NRA) % OB::NR, s, slot);
+  };
+  // Matrix instructions of register set `set`, interleaved with the reads of quarter s_next (slot) into
+  // the other set (RD) and with the loads of stage ks (LD). The operands swap places, so a lane holds
+  // one output row and, in runs of four accumulators, four neighbouring columns.
+  auto quarter = [&](int set, int s_next, uint32_t slot, int ks, auto rd, auto ld) {
+    constexpr bool RD = decltype(rd)::value, LD = decltype(ld)::value;
+    constexpr int NM = FM * FN;
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      acc[m / FN][m % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          __builtin_bit_cast(bf16x8, fb[set][m % FN]), __builtin_bit_cast(bf16x8, fa[set][m / FN]), acc[m / FN][m % FN],
+          0, 0, 0);
+      if (RD) {
+#pragma unroll
+        for (int r = m * NR / NM; r < (m + 1) * NR / NM; ++r) read(r, s_next, 1 - set, slot);
+      }
+      if (LD) {
+#pragma unroll
+        for (int i = m * NL / NM; i < (m + 1) * NL / NM; ++i) issue(i, ks);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+
+  if (KT > 0) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) issue(i, 0);
+    advance();
+  }
+  if (KT > 1) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) issue(i, 1);
+    advance();
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  if (KT > 0) {
+    if (KT > 1)
+      wait_vmcnt<NL>();
+    else
+      wait_vmcnt<0>();
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read(r, 0, 0, 0);
+  }
+  auto stage = [&](int kt, auto more, auto load) {  // MORE: stage kt + 1 exists; LOAD: stage kt + 2 does
+    const uint32_t slot = (uint32_t)(kt & 1) * S::SLOT, next = S::SLOT - slot;
+    quarter(0, 1, slot, 0, Y(), N());
+    quarter(1, 2, slot, 0, Y(), N());
+    quarter(0, 3, slot, 0, Y(), N());
+    if (decltype(more)::value) {
+      wait_vmcnt<0>();  // stage kt + 1 has landed (its loads are a stage old)
+      __syncthreads();  // for every wavefront, and none reads this stage's slot any more
+    }
+    quarter(1, 0, next, kt + 2, more, load);
+    if (decltype(load)::value) advance();
+  };
+  int kt = 0;
+  for (; kt + 2 < KT; ++kt) stage(kt, Y(), Y());
+  if (kt + 1 < KT) {
+    stage(kt, Y(), N());
+    ++kt;
+  }
+  if (kt < KT) stage(kt, N(), N());
+  __syncthreads();  // the slots become the epilogue's staging
+
+  // Epilogue: the tile goes through LDS so that stores are 16-byte runs along output rows.
+  const int r32 = lane & 31, g = lane >> 5;
+  if constexpr (!F32) {
+    uint16_t* cs = reinterpret_cast<uint16_t*>(smem);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        asm volatile("" : "+a"(acc[i][j]));  // fragments leave the AGPRs one at a time
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint2*>(cs + (wm * (BM / 2) + i * 32 + r32) * S::PITCH16 + wn * (BN / 2) + j * 32 + 8 * c + 4 * g) =
+              make_uint2(bf16x2_bits(acc[i][j][4 * c], acc[i][j][4 * c + 1]),
+                         bf16x2_bits(acc[i][j][4 * c + 2], acc[i][j][4 * c + 3]));
+      }
+    __syncthreads();
+    constexpr int CPR = BN / 8;
+#pragma unroll 2
+    for (int t = tid; t < BM * CPR; t += 256) {
+      const int r = t / CPR, c = t % CPR * 8;
+      if (r < mr && c < nc)
+        store16_nt(reinterpret_cast<uint16_t*>(p.c) + c_base + (int64_t)r * p.ldc + c,
+                   *reinterpret_cast<const uint4*>(cs + r * S::PITCH16 + c));
+    }
+    return;
+  }
+  float* cs = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {  // half the rows at a time
+    if (half) __syncthreads();
+    if (wm == half) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float4*>(cs + (i * 32 + r32) * S::PITCH32 + wn * (BN / 2) + j * 32 + 8 * c + 4 * g) =
+                make_float4(acc[i][j][4 * c], acc[i][j][4 * c + 1], acc[i][j][4 * c + 2], acc[i][j][4 * c + 3]);
+        }
+    }
+    __syncthreads();
+    constexpr int CPR = BN / 4;
+#pragma unroll 2
+    for (int t = tid; t < BM / 2 * CPR; t += 256) {
+      const int r = t / CPR, c = t % CPR * 4, row = half * (BM / 2) + r;
+      if (row < mr && c < nc) {
+        float4 v = *reinterpret_cast<const float4*>(cs + r * S::PITCH32 + c);
+        float* o = reinterpret_cast<float*>(p.c) + c_base + (int64_t)row * p.ldc + c;
+        if (p.accum) {
+          const float4 u = *reinterpret_cast<const float4*>(o);
+          v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        }
+        store16_nt(o, __builtin_bit_cast(uint4, v));
+      }
+    }
+  }
+}
+
+// Position of block b of n (a contiguous run of positions per XCD: blocks go to the 8 XCDs in turn).
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
+  const uint32_t q = n / 8, r = n % 8, x = b % 8;
+  return (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + b / 8;
+}
+
+// OP 0 and 1: row tiles in groups of GM, all column tiles of a group before the next, so that the tiles
+// in flight on an XCD share x rows and w columns in its L2.
+template <int OP, int BM, int BN, bool F32>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_rows_kernel(GroupedParams p, int col_tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN>::LDS];
+  const RowTiles rt = count_row_tiles(p.offs, p.E, p.M, BM);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = rt.ok ? 0 : 1;
+  if (!rt.ok) return;
+  const uint32_t total = (uint32_t)rt.tiles * (uint32_t)col_tiles;
+  if (blockIdx.x >= total) return;
+  const uint32_t pos = xcd_run(blockIdx.x, total);
+  constexpr uint32_t GM = 4;
+  const uint32_t per = GM * (uint32_t)col_tiles, grp = pos / per, in = pos - grp * per;
+  const uint32_t rows = min(GM, (uint32_t)rt.tiles - grp * GM);
+  const RowTile r = find_row_tile(rt, p.offs, p.E, BM, (int)(grp * GM + in % rows));
+  const int64_t n0 = (int64_t)(in / rows) * BN;
+  const int64_t on = OP == 0 ? p.N : p.K;
+  const uint16_t* w = p.b + (int64_t)r.e * p.N * p.K;
+  grouped_tile<OP, BM, BN, F32>(p, smem, p.a + r.m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, r.m0 * p.ldc + n0,
+                           r.m1 - r.m0, (int)min(on - n0, (int64_t)BN), (int)(OP == 0 ? p.K : p.N));
+}
+
+// OP 2: one grid of output tiles per expert, experts with the most rows first (their blocks run longest),
+// in index order past 64 experts.
+template <int BM, int BN, bool F32>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_dw_kernel(GroupedParams p, int row_tiles, int col_tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN>::LDS];
+  const bool ok = ragged_ok(p.offs, p.E, p.M);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = ok ? 0 : 1;
+  if (!ok) return;
+  const uint32_t per = (uint32_t)row_tiles * (uint32_t)col_tiles;
+  const int place = (int)(blockIdx.x / per);
+  int e = place;
+  if (p.E <= 64) {
+    const int lane = threadIdx.x & 63;
+    const int n = lane < p.E ? p.offs[lane + 1] - p.offs[lane] : -1;
+    int rank = 0;
+    for (int j = 0; j < p.E; ++j) {
+      const int nj = __builtin_amdgcn_readlane(n, j);
+      rank += nj > n || (nj == n && j < lane);
+    }
+    e = __ffsll((unsigned long long)__ballot(lane < p.E && rank == place)) - 1;
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int c0 = p.offs[e], c1 = p.offs[e + 1];
+  const uint32_t pos = xcd_run(blockIdx.x % per, per);
+  const int64_t m0 = (int64_t)(pos / (uint32_t)col_tiles) * BM, n0 = (int64_t)(pos % (uint32_t)col_tiles) * BN;
+  if (p.accum && c1 == c0) return;  // nothing to add
+  grouped_tile<2, BM, BN, F32>(p, smem, p.a + (int64_t)c0 * p.lda + m0, p.b + (int64_t)c0 * p.ldb + n0, p.ldb,
+                          (int64_t)e * p.N * p.K + m0 * p.ldc + n0, (int)min(p.N - m0, (int64_t)BM),
+                          (int)min(p.K - n0, (int64_t)BN), c1 - c0);
+}
+
 }  // namespace mxf
+
+namespace {
+
+bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <int OP, int BM, int BN, bool F32>
+hipError_t launch_tiles_as(const mxf::GroupedParams& p, hipStream_t st) {
+  const int64_t on = OP == 0 ? p.N : p.K, ct = (on + BN - 1) / BN;
+  if constexpr (OP == 2) {
+    const int64_t rt = (p.N + BM - 1) / BM;
+    hipLaunchKernelGGL((mxf::grouped_dw_kernel<BM, BN, F32>), dim3((unsigned)(p.E * rt * ct)), dim3(256), 0, st, p, (int)rt,
+                       (int)ct);
+  } else {
+    int64_t rt = p.M / BM + (p.E < p.M ? p.E : p.M);  // every expert may end inside a tile
+    if (rt == 0) rt = 1;                              // (one block looks at the offsets)
+    hipLaunchKernelGGL((mxf::grouped_rows_kernel<OP, BM, BN, F32>), dim3((unsigned)(rt * ct)), dim3(256), 0, st, p, (int)ct);
+  }
+  return hipGetLastError();
+}
+
+template <int OP, int BM, int BN>
+hipError_t launch_tiles(const mxf::GroupedParams& p, hipStream_t st) {
+  return p.out_f32 ? launch_tiles_as<OP, BM, BN, true>(p, st) : launch_tiles_as<OP, BM, BN, false>(p, st);
+}
+
+}  // namespace
 
 hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipStream_t st) {
   using namespace mxf;
-  (void)ncu;
-  const int64_t on = op == 0 ? p.N : p.K;
+  const int64_t om = op == 2 ? p.N : p.M, on = op == 0 ? p.N : p.K;
+  // 16-byte rows, and offsets inside a tile that a descriptor covers (256 rows of ld elements < 2 GB)
+  const bool aligned = p.N % 8 == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && p.ldb % 8 == 0 &&
+                       p.ldc % (p.out_f32 ? 4 : 8) == 0 && a16(p.a) && a16(p.b) && a16(p.c) && p.lda < (1 << 22) &&
+                       p.ldb < (1 << 22) && !p.bq;
+  if (aligned) {
+    // 256 x 256 tiles where they fill the chip
+    const int64_t big = (op == 2 ? p.E * ((om + 255) / 256) : (om + 255) / 256) * ((on + 255) / 256);
+    const bool b256 = big >= ncu;
+    if (op == 0) return b256 ? launch_tiles<0, 256, 256>(p, st) : launch_tiles<0, 128, 128>(p, st);
+    if (op == 1) return b256 ? launch_tiles<1, 256, 256>(p, st) : launch_tiles<1, 128, 128>(p, st);
+    return b256 ? launch_tiles<2, 256, 256>(p, st) : launch_tiles<2, 128, 128>(p, st);
+  }
   const int64_t ct = (on + AT - 1) / AT;
-  const int64_t rt = op == 2 ? p.E * ((p.N + AT - 1) / AT) : p.M / AT + (p.E < p.M ? p.E : p.M);
-  const int64_t blocks = rt * ct;
-  if (blocks == 0) return hipSuccess;
-  if (blocks > 0xFFFFFF) return hipErrorInvalidValue;  // fewer than 2^32 threads
-  const dim3 g((unsigned)blocks), b(256);
+  int64_t rt = op == 2 ? p.E * ((om + AT - 1) / AT) : p.M / AT + (p.E < p.M ? p.E : p.M);
+  if (rt == 0) rt = 1;
+  const dim3 g((unsigned)(rt * ct)), b(256);
   if (op == 0)
     hipLaunchKernelGGL((grouped_any_kernel<0, false>), g, b, 0, st, p, ct);
   else if (op == 1)

@@ -181,6 +181,27 @@ __device__ __forceinline__ void dswiglu2(uint32_t dh2, uint32_t g2, uint32_t u2,
   du2 = bf16x2_bits(du0, du1);
 }
 
+// s_waitcnt with only the vector-memory counter constrained (gfx9 encoding: vmcnt low bits
+// [3:0] and high bits [15:14]; expcnt 7 and lgkmcnt 15 mean "no wait").
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt out of range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(lds_ptr)p;
+}
+
+// LDS reads through a 32-bit LDS byte address; constant offsets added to the returned pointer
+// fold into the instruction's offset field.
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) const u32x4_t lds_u4;
+typedef __attribute__((address_space(3))) const uint8_t lds_u8;
+__device__ __forceinline__ lds_u4* lds16_at(uint32_t a) { return (lds_u4*)(uintptr_t)a; }
+__device__ __forceinline__ lds_u8* lds8_at(uint32_t a) { return (lds_u8*)(uintptr_t)a; }
+
 // Device-side check of the token-offset contract, done by one whole wavefront; every lane
 // returns the same answer. offs [E+1], counts [E] or null.
 __device__ __forceinline__ bool offsets_valid(const int32_t* offs, const int32_t* counts, int E,
