@@ -191,10 +191,13 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedParams p, int64
 // Block tile BM x BN, four wavefronts in a 2 x 2 grid, each owning a (BM/2) x (BN/2) tile of 32 x 32
 // matrix-core fragments (256 x 256: all 256 accumulators of a lane in AGPRs, one block per CU).
 //
-// The contraction advances 64 at a time through two LDS slots filled by direct global->LDS loads of
-// 1 KB. In a stage the 16-deep matrix instructions of one quarter run beside the LDS reads of the
-// next quarter; before the last quarter one wait and one barrier make the next stage visible and this
-// stage's slot free, and the last quarter issues the loads of the stage after the next into it.
+// The contraction advances 64 at a time (128-byte rows: whole cache lines). A stage's share of one
+// operand is a unit; five units fill the LDS, which direct global->LDS loads of 1 KB fill in the order
+// A0 B0 A1 B1 A2 B2 ... A stage is four 16-deep quarters; the matrix instructions of one run beside the
+// LDS reads of the next. Before the last quarter one wait and one barrier make the next stage visible and
+// this stage's two units free: B of stage + 2 and A of stage + 3 follow into them, one load per four matrix
+// instructions over the next four quarters, so the vector-memory pipe never takes a burst. Loads past
+// the last stage ask for no element (below), which keeps every stage the same.
 //
 // An operand is stored in LDS as it lies in memory:
 //   contraction-contiguous (x and dy of OP 0, 1; w of OP 0): rows of 64 elements (128 bytes), fragments
@@ -225,10 +228,6 @@ __device__ __forceinline__ void buffer_to_lds(i32x4 rsrc, uint32_t voff, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
-__device__ __forceinline__ i32x4 descriptor(uint64_t base) {
-  return (i32x4){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xFFFFu), (int)kNoElement, 0x00020000};
-}
-
 // One operand of a tile: R rows or columns of the output, contraction-contiguous (KC) or not.
 template <bool KC, int R>
 struct Operand {
@@ -236,7 +235,7 @@ struct Operand {
   static constexpr int CPR = R / 8;            // contraction-slow: 16-byte chunks per row
   static constexpr int RPL = 64 / CPR;         // and rows per load
   static constexpr int NR = KC ? 1 : 2;        // LDS reads per fragment
-  uint64_t base;      // first element of the stage to load next
+  i32x4 rsrc;         // from the first element of the stage to load next
   uint64_t step;      // bytes between stages
   uint32_t voff[NLOAD];
   uint32_t k_lane;    // contraction index of the lane's first element: KC: of even loads, else of load 0
@@ -246,7 +245,8 @@ struct Operand {
   // this wavefront's first row or column; lds: the operand's place in slot 0
   __device__ __forceinline__ void init(const uint16_t* origin, int64_t ld, int valid, int wid, int w0, uint32_t lds) {
     const int l = threadIdx.x & 63;
-    base = uniform64((uint64_t)origin);
+    const uint64_t base = uniform64((uint64_t)origin);
+    rsrc = (i32x4){(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)kNoElement, 0x00020000};
     step = KC ? 128 : (uint64_t)ld * 128;
     const uint32_t ldb = (uint32_t)ld * 2;
 #pragma unroll
@@ -272,11 +272,16 @@ struct Operand {
       }
     }
   }
-  // Load i of the stage at `base`, of which `left` contraction indexes exist, into LDS.
+  // Load i of the stage at `rsrc`, of which `left` contraction indexes exist, into LDS.
   __device__ __forceinline__ void load(int i, int left, uint32_t lds) const {
     // odd loads of a contraction-contiguous operand start four rows further, which flips chunk bit 2
     const int k = KC ? (int)(k_lane ^ (32 * (i & 1))) : (int)k_lane + RPL * i;
-    buffer_to_lds(descriptor(base), k < left ? voff[i] : kNoElement, lds + i * 1024);
+    buffer_to_lds(rsrc, k < left ? voff[i] : kNoElement, lds + i * 1024);
+  }
+  __device__ __forceinline__ void advance() {
+    const uint64_t b = ((uint64_t)(uint32_t)rsrc[1] << 32 | (uint32_t)rsrc[0]) + step;  // (48-bit addresses: no stride bits)
+    rsrc[0] = (int)(uint32_t)b;
+    rsrc[1] = (int)(uint32_t)(b >> 32);
   }
   // Part h of fragment i in quarter s.
   __device__ __forceinline__ void read(u32x4_t& f, int i, int h, int s, uint32_t slot) const {
@@ -295,12 +300,12 @@ struct Operand {
 template <int BM, int BN>
 struct TileSize {
   static constexpr int FM = BM / 64, FN = BN / 64;
-  static constexpr int B_OFF = BM * 128;         // of a slot
-  static constexpr int SLOT = (BM + BN) * 128;
+  static constexpr int UNIT = BM * 128;          // bytes of an operand's stage
+  static_assert(BM == BN, "units of one size");
   static constexpr int PITCH16 = BN + 8, PITCH32 = BN + 4;  // epilogue staging rows (elements)
   static constexpr int EPI16 = BM * PITCH16 * 2, EPI32 = BM / 2 * PITCH32 * 4;
   static constexpr int max3(int a, int b, int c) { return a > b ? (a > c ? a : c) : (b > c ? b : c); }
-  static constexpr int LDS = max3(2 * SLOT, EPI16, EPI32);
+  static constexpr int LDS = max3(5 * UNIT, EPI16, EPI32);
 };
 
 // Output rows [m0, m0 + mr) and columns [n0, n0 + nc) of the tile, contraction length kc; a and b: the
@@ -319,67 +324,65 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   OA oa;
   OB ob;
   oa.init(a, p.lda, mr, wid, wm * (BM / 2), lds0);
-  ob.init(b, ldb, nc, wid, wn * (BN / 2), lds0 + S::B_OFF);
-  const uint32_t lds_a = lds0 + wid_u * OA::NLOAD * 1024, lds_b = lds0 + S::B_OFF + wid_u * OB::NLOAD * 1024;
+  ob.init(b, ldb, nc, wid, wn * (BN / 2), lds0);
+  const uint32_t lds_w = lds0 + wid_u * OA::NLOAD * 1024;  // this wavefront's part of unit 0
   const int KT = (kc + 63) >> 6;
-
-  constexpr int NL = OA::NLOAD + OB::NLOAD;
-  auto issue = [&](int i, int ks) {  // load i of stage ks, whose first elements oa.base and ob.base point at
-    const int left = kc - ks * 64;
-    const uint32_t slot = (uint32_t)(ks & 1) * S::SLOT;
-    if (i < OA::NLOAD)
-      oa.load(i, left, lds_a + slot);
-    else
-      ob.load(i - OA::NLOAD, left, lds_b + slot);
-  };
-  auto advance = [&]() {
-    oa.base += oa.step;
-    ob.base += ob.step;
-  };
+  constexpr int NL = OA::NLOAD;  // loads of a unit per wavefront
 
   f32x16 acc[FM][FN];
   u32x4_t fa[2][FM], fb[2][FN];
   constexpr int NRA = FM * OA::NR, NR = NRA + FN * OB::NR;  // LDS reads of a quarter
-  auto read = [&](int r, int s, int set, uint32_t slot) {
+  auto read = [&](int r, int s, int set, uint32_t ua, uint32_t ub) {
     if (r < NRA)
-      oa.read(fa[set][r / OA::NR], r / OA::NR, r % OA::NR, s, slot);
+      oa.read(fa[set][r / OA::NR], r / OA::NR, r % OA::NR, s, ua);
     else
-      ob.read(fb[set][(r - NRA) / OB::NR], (r - NRA) / OB::NR, (r - NRA) % OB::NR, s, slot);
+      ob.read(fb[set][(r - NRA) / OB::NR], (r - NRA) / OB::NR, (r - NRA) % OB::NR, s, ub);
   };
-  // Matrix instructions of register set `set`, interleaved with the reads of quarter s_next (slot) into
-  // the other set (RD) and with the loads of stage ks (LD). The operands swap places, so a lane holds
-  // one output row and, in runs of four accumulators, four neighbouring columns.
-  auto quarter = [&](int set, int s_next, uint32_t slot, int ks, auto rd, auto ld) {
-    constexpr bool RD = decltype(rd)::value, LD = decltype(ld)::value;
-    constexpr int NM = FM * FN;
+  // Matrix instructions of quarter s (register set s % 2), interleaved with the reads of the next quarter
+  // (units ua, ub) and with half a unit of loads: quarter 3: B's first, 0: B's second, 1 and 2: A's halves.
+  // The operands swap places, so a lane holds one output row and, in runs of four accumulators, four
+  // neighbouring columns.
+  auto quarter = [&](auto s_, uint32_t ua, uint32_t ub, int left, uint32_t ld) {
+    constexpr int s = decltype(s_)::value, set = s & 1;
+    constexpr int NM = FM * FN, NH = NM / 2, NQ = NL / 2;
+    constexpr int L0 = s == 0 || s == 2 ? NQ : 0;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       acc[m / FN][m % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
           __builtin_bit_cast(bf16x8, fb[set][m % FN]), __builtin_bit_cast(bf16x8, fa[set][m / FN]), acc[m / FN][m % FN],
           0, 0, 0);
-      if (RD) {
+      if (m < NH) {
 #pragma unroll
-        for (int r = m * NR / NM; r < (m + 1) * NR / NM; ++r) read(r, s_next, 1 - set, slot);
+        for (int r = m * NR / NH; r < (m + 1) * NR / NH; ++r) read(r, (s + 1) & 3, 1 - set, ua, ub);
       }
-      if (LD) {
 #pragma unroll
-        for (int i = m * NL / NM; i < (m + 1) * NL / NM; ++i) issue(i, ks);
+      for (int i = L0 + m * NQ / NM; i < L0 + (m + 1) * NQ / NM; ++i) {
+        if (s == 3 || s == 0)
+          ob.load(i, left, ld);
+        else
+          oa.load(i, left, ld);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  using Y = std::true_type;
-  using N = std::false_type;
+  using Q0 = std::integral_constant<int, 0>;
+  using Q1 = std::integral_constant<int, 1>;
+  using Q2 = std::integral_constant<int, 2>;
+  using Q3 = std::integral_constant<int, 3>;
+  constexpr uint32_t U = S::UNIT;
 
-  if (KT > 0) {
+  if (KT > 0) {  // A0 B0 A1 and half of B1
 #pragma unroll
-    for (int i = 0; i < NL; ++i) issue(i, 0);
-    advance();
-  }
-  if (KT > 1) {
+    for (int i = 0; i < NL; ++i) oa.load(i, kc, lds_w);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) issue(i, 1);
-    advance();
+    for (int i = 0; i < NL; ++i) ob.load(i, kc, lds_w + U);
+    oa.advance();
+    ob.advance();
+#pragma unroll
+    for (int i = 0; i < NL; ++i) oa.load(i, kc - 64, lds_w + 2 * U);
+    oa.advance();
+#pragma unroll
+    for (int i = 0; i < NL / 2; ++i) ob.load(i, kc - 64, lds_w + 3 * U);
   }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -389,33 +392,31 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   if (KT > 0) {
-    if (KT > 1)
-      wait_vmcnt<NL>();
-    else
-      wait_vmcnt<0>();
+    wait_vmcnt<NL + NL / 2>();  // stage 0 has landed
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < NR; ++r) read(r, 0, 0, 0);
-  }
-  auto stage = [&](int kt, auto more, auto load) {  // MORE: stage kt + 1 exists; LOAD: stage kt + 2 does
-    const uint32_t slot = (uint32_t)(kt & 1) * S::SLOT, next = S::SLOT - slot;
-    quarter(0, 1, slot, 0, Y(), N());
-    quarter(1, 2, slot, 0, Y(), N());
-    quarter(0, 3, slot, 0, Y(), N());
-    if (decltype(more)::value) {
-      wait_vmcnt<0>();  // stage kt + 1 has landed (its loads are a stage old)
-      __syncthreads();  // for every wavefront, and none reads this stage's slot any more
+    for (int r = 0; r < NR; ++r) read(r, 0, 0, 0, U);
+    uint32_t ua = 0, ub = U;                    // units of stage kt
+    uint32_t pa = lds_w + 3 * U, pb = lds_w + 4 * U;  // where B of stage kt + 1 and A of stage kt + 2 go
+    int left = kc - 64;
+#pragma unroll 1
+    for (int kt = 0; kt < KT; ++kt) {
+      quarter(Q0(), ua, ub, left, pa);
+      ob.advance();
+      left -= 64;
+      quarter(Q1(), ua, ub, left, pb);
+      quarter(Q2(), ua, ub, left, pb);
+      oa.advance();
+      wait_vmcnt<NL>();  // all but A of stage kt + 2 has landed
+      __syncthreads();   // for every wavefront, and none reads this stage's units any more
+      pa = lds_w + ua;
+      pb = lds_w + ub;
+      ua = ua >= 3 * U ? ua - 3 * U : ua + 2 * U;
+      ub = ub >= 3 * U ? ub - 3 * U : ub + 2 * U;
+      quarter(Q3(), ua, ub, left, pa);
     }
-    quarter(1, 0, next, kt + 2, more, load);
-    if (decltype(load)::value) advance();
-  };
-  int kt = 0;
-  for (; kt + 2 < KT; ++kt) stage(kt, Y(), Y());
-  if (kt + 1 < KT) {
-    stage(kt, Y(), N());
-    ++kt;
+    wait_vmcnt<0>();  // no load may still target LDS
   }
-  if (kt < KT) stage(kt, N(), N());
   __syncthreads();  // the slots become the epilogue's staging
 
   // Epilogue: the tile goes through LDS so that stores are 16-byte runs along output rows.
