@@ -300,8 +300,7 @@ struct Operand {
 template <int BM, int BN>
 struct TileSize {
   static constexpr int FM = BM / 64, FN = BN / 64;
-  static constexpr int UNIT = BM * 128;          // bytes of an operand's stage
-  static_assert(BM == BN, "units of one size");
+  static constexpr int UNIT = (BM > BN ? BM : BN) * 128;  // bytes of an operand's stage
   static constexpr int PITCH16 = BN + 8, PITCH32 = BN + 4;  // epilogue staging rows (elements)
   static constexpr int EPI16 = BM * PITCH16 * 2, EPI32 = BM / 2 * PITCH32 * 4;
   static constexpr int max3(int a, int b, int c) { return a > b ? (a > c ? a : c) : (b > c ? b : c); }
@@ -325,9 +324,9 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   OB ob;
   oa.init(a, p.lda, mr, wid, wm * (BM / 2), lds0);
   ob.init(b, ldb, nc, wid, wn * (BN / 2), lds0);
-  const uint32_t lds_w = lds0 + wid_u * OA::NLOAD * 1024;  // this wavefront's part of unit 0
+  constexpr int NLA = OA::NLOAD, NLB = OB::NLOAD;  // loads of a unit per wavefront
+  const uint32_t lds_a = lds0 + wid_u * NLA * 1024, lds_b = lds0 + wid_u * NLB * 1024;  // its part of unit 0
   const int KT = (kc + 63) >> 6;
-  constexpr int NL = OA::NLOAD;  // loads of a unit per wavefront
 
   f32x16 acc[FM][FN];
   u32x4_t fa[2][FM], fb[2][FN];
@@ -344,7 +343,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   // neighbouring columns.
   auto quarter = [&](auto s_, uint32_t ua, uint32_t ub, int left, uint32_t ld) {
     constexpr int s = decltype(s_)::value, set = s & 1;
-    constexpr int NM = FM * FN, NH = NM / 2, NQ = NL / 2;
+    constexpr int NM = FM * FN, NH = NM / 2, NQ = (s == 0 || s == 3 ? NLB : NLA) / 2;
     constexpr int L0 = s == 0 || s == 2 ? NQ : 0;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
@@ -373,16 +372,16 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
 
   if (KT > 0) {  // A0 B0 A1 and half of B1
 #pragma unroll
-    for (int i = 0; i < NL; ++i) oa.load(i, kc, lds_w);
+    for (int i = 0; i < NLA; ++i) oa.load(i, kc, lds_a);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) ob.load(i, kc, lds_w + U);
+    for (int i = 0; i < NLB; ++i) ob.load(i, kc, lds_b + U);
     oa.advance();
     ob.advance();
 #pragma unroll
-    for (int i = 0; i < NL; ++i) oa.load(i, kc - 64, lds_w + 2 * U);
+    for (int i = 0; i < NLA; ++i) oa.load(i, kc - 64, lds_a + 2 * U);
     oa.advance();
 #pragma unroll
-    for (int i = 0; i < NL / 2; ++i) ob.load(i, kc - 64, lds_w + 3 * U);
+    for (int i = 0; i < NLB / 2; ++i) ob.load(i, kc - 64, lds_b + 3 * U);
   }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -392,12 +391,12 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   if (KT > 0) {
-    wait_vmcnt<NL + NL / 2>();  // stage 0 has landed
+    wait_vmcnt<NLA + NLB / 2>();  // stage 0 has landed
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < NR; ++r) read(r, 0, 0, 0, U);
     uint32_t ua = 0, ub = U;                    // units of stage kt
-    uint32_t pa = lds_w + 3 * U, pb = lds_w + 4 * U;  // where B of stage kt + 1 and A of stage kt + 2 go
+    uint32_t pa = lds_b + 3 * U, pb = lds_a + 4 * U;  // where B of stage kt + 1 and A of stage kt + 2 go
     int left = kc - 64;
 #pragma unroll 1
     for (int kt = 0; kt < KT; ++kt) {
@@ -407,10 +406,10 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
       quarter(Q1(), ua, ub, left, pb);
       quarter(Q2(), ua, ub, left, pb);
       oa.advance();
-      wait_vmcnt<NL>();  // all but A of stage kt + 2 has landed
+      wait_vmcnt<NLA>();  // all but A of stage kt + 2 has landed
       __syncthreads();   // for every wavefront, and none reads this stage's units any more
-      pa = lds_w + ua;
-      pb = lds_w + ub;
+      pa = lds_b + ua;
+      pb = lds_a + ub;
       ua = ua >= 3 * U ? ua - 3 * U : ua + 2 * U;
       ub = ub >= 3 * U ? ub - 3 * U : ub + 2 * U;
       quarter(Q3(), ua, ub, left, pa);
@@ -486,25 +485,65 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
 }
 
 // OP 0 and 1: row tiles in groups of GM, all column tiles of a group before the next, so that the tiles
-// in flight on an XCD share x rows and w columns in its L2.
+// in flight on an XCD share rows of x and columns of w in its L2.
+//
+// Of T tiles on C compute units the last T mod C would leave most of the chip idle for a whole tile's time:
+// they are split into four quarters, or two halves of the rows, where that many fit the chip at once. Their
+// blocks come first (lowest ids). A tile whose expert ends within its first 128 rows runs as a half.
 template <int OP, int BM, int BN, bool F32>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_rows_kernel(GroupedParams p, int col_tiles) {
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_rows_kernel(GroupedParams p, int col_tiles, int ncu) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN>::LDS];
   const RowTiles rt = count_row_tiles(p.offs, p.E, p.M, BM);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = rt.ok ? 0 : 1;
   if (!rt.ok) return;
   const uint32_t total = (uint32_t)rt.tiles * (uint32_t)col_tiles;
-  if (blockIdx.x >= total) return;
-  const uint32_t pos = xcd_run(blockIdx.x, total);
+  uint32_t pos, part = 0, split = 1;
+  if constexpr (BM == 256) {
+    const uint32_t rem = total % (uint32_t)ncu, full = total - rem;
+    split = 4 * rem <= (uint32_t)ncu ? 4 : 2 * rem <= (uint32_t)ncu ? 2 : 1;
+    const uint32_t first = split == 1 ? 0 : (rem * split + 7) & ~7u;  // (a multiple of 8 keeps block id % 8 the XCD)
+    if (blockIdx.x < first) {
+      if (blockIdx.x >= rem * split) return;
+      pos = full + blockIdx.x / split;
+      part = blockIdx.x % split;
+    } else {
+      const uint32_t n = split == 1 ? total : full;
+      if (blockIdx.x - first >= n) return;
+      pos = xcd_run(blockIdx.x - first, n);
+      split = 1;
+    }
+  } else {
+    if (blockIdx.x >= total) return;
+    pos = xcd_run(blockIdx.x, total);
+  }
   constexpr uint32_t GM = 4;
   const uint32_t per = GM * (uint32_t)col_tiles, grp = pos / per, in = pos - grp * per;
   const uint32_t rows = min(GM, (uint32_t)rt.tiles - grp * GM);
   const RowTile r = find_row_tile(rt, p.offs, p.E, BM, (int)(grp * GM + in % rows));
-  const int64_t n0 = (int64_t)(in / rows) * BN;
-  const int64_t on = OP == 0 ? p.N : p.K;
+  int64_t n0 = (int64_t)(in / rows) * BN;
+  const int64_t on = OP == 0 ? p.N : p.K, kc = OP == 0 ? p.K : p.N;
   const uint16_t* w = p.b + (int64_t)r.e * p.N * p.K;
-  grouped_tile<OP, BM, BN, F32>(p, smem, p.a + r.m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, r.m0 * p.ldc + n0,
-                           r.m1 - r.m0, (int)min(on - n0, (int64_t)BN), (int)(OP == 0 ? p.K : p.N));
+  int m0 = r.m0, mr = r.m1 - r.m0;
+  if constexpr (BM == 256) {
+    if (split > 1) {
+      m0 += (int)(part >> (split == 4)) * 128;
+      mr = min(r.m1 - m0, 128);
+      if (split == 4) n0 += (part & 1) * 128;
+      if (mr <= 0 || n0 >= on) return;
+    }
+    if (split == 4) {
+      grouped_tile<OP, 128, 128, F32>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, m0 * p.ldc + n0,
+                                      mr, (int)min(on - n0, (int64_t)128), (int)kc);
+      return;
+    }
+    if (mr <= 128) {
+      grouped_tile<OP, 128, 256, F32>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, m0 * p.ldc + n0,
+                                      mr, (int)min(on - n0, (int64_t)256), (int)kc);
+      return;
+    }
+  }
+  grouped_tile<OP, BM, BN, F32>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, m0 * p.ldc + n0, mr,
+                                (int)min(on - n0, (int64_t)BN), (int)kc);
 }
 
 // OP 2: one grid of output tiles per expert, experts with the most rows first (their blocks run longest),
@@ -531,7 +570,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_dw_kernel(Grou
   e = __builtin_amdgcn_readfirstlane(e);
   const int c0 = p.offs[e], c1 = p.offs[e + 1];
   const uint32_t pos = xcd_run(blockIdx.x % per, per);
-  const int64_t m0 = (int64_t)(pos / (uint32_t)col_tiles) * BM, n0 = (int64_t)(pos % (uint32_t)col_tiles) * BN;
+  // (row tiles in groups, as above)
+  constexpr uint32_t GM = 4;
+  const uint32_t grp = pos / (GM * (uint32_t)col_tiles), in = pos - grp * (GM * (uint32_t)col_tiles);
+  const uint32_t rows = min(GM, (uint32_t)row_tiles - grp * GM);
+  const int64_t m0 = (int64_t)(grp * GM + in % rows) * BM, n0 = (int64_t)(in / rows) * BN;
   if (p.accum && c1 == c0) return;  // nothing to add
   grouped_tile<2, BM, BN, F32>(p, smem, p.a + (int64_t)c0 * p.lda + m0, p.b + (int64_t)c0 * p.ldb + n0, p.ldb,
                           (int64_t)e * p.N * p.K + m0 * p.ldc + n0, (int)min(p.N - m0, (int64_t)BM),
@@ -545,7 +588,7 @@ namespace {
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <int OP, int BM, int BN, bool F32>
-hipError_t launch_tiles_as(const mxf::GroupedParams& p, hipStream_t st) {
+hipError_t launch_tiles_as(const mxf::GroupedParams& p, int ncu, hipStream_t st) {
   const int64_t on = OP == 0 ? p.N : p.K, ct = (on + BN - 1) / BN;
   if constexpr (OP == 2) {
     const int64_t rt = (p.N + BM - 1) / BM;
@@ -554,14 +597,15 @@ hipError_t launch_tiles_as(const mxf::GroupedParams& p, hipStream_t st) {
   } else {
     int64_t rt = p.M / BM + (p.E < p.M ? p.E : p.M);  // every expert may end inside a tile
     if (rt == 0) rt = 1;                              // (one block looks at the offsets)
-    hipLaunchKernelGGL((mxf::grouped_rows_kernel<OP, BM, BN, F32>), dim3((unsigned)(rt * ct)), dim3(256), 0, st, p, (int)ct);
+    hipLaunchKernelGGL((mxf::grouped_rows_kernel<OP, BM, BN, F32>), dim3((unsigned)(rt * ct + (BM == 256 ? ncu : 0))), dim3(256), 0,
+                       st, p, (int)ct, ncu);  // (+ ncu: the blocks of split tiles)
   }
   return hipGetLastError();
 }
 
 template <int OP, int BM, int BN>
-hipError_t launch_tiles(const mxf::GroupedParams& p, hipStream_t st) {
-  return p.out_f32 ? launch_tiles_as<OP, BM, BN, true>(p, st) : launch_tiles_as<OP, BM, BN, false>(p, st);
+hipError_t launch_tiles(const mxf::GroupedParams& p, int ncu, hipStream_t st) {
+  return p.out_f32 ? launch_tiles_as<OP, BM, BN, true>(p, ncu, st) : launch_tiles_as<OP, BM, BN, false>(p, ncu, st);
 }
 
 }  // namespace
@@ -577,9 +621,9 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
     // 256 x 256 tiles where they fill the chip
     const int64_t big = (op == 2 ? p.E * ((om + 255) / 256) : (om + 255) / 256) * ((on + 255) / 256);
     const bool b256 = big >= ncu;
-    if (op == 0) return b256 ? launch_tiles<0, 256, 256>(p, st) : launch_tiles<0, 128, 128>(p, st);
-    if (op == 1) return b256 ? launch_tiles<1, 256, 256>(p, st) : launch_tiles<1, 128, 128>(p, st);
-    return b256 ? launch_tiles<2, 256, 256>(p, st) : launch_tiles<2, 128, 128>(p, st);
+    if (op == 0) return b256 ? launch_tiles<0, 256, 256>(p, ncu, st) : launch_tiles<0, 128, 128>(p, ncu, st);
+    if (op == 1) return b256 ? launch_tiles<1, 256, 256>(p, ncu, st) : launch_tiles<1, 128, 128>(p, ncu, st);
+    return b256 ? launch_tiles<2, 256, 256>(p, ncu, st) : launch_tiles<2, 128, 128>(p, ncu, st);
   }
   const int64_t ct = (on + AT - 1) / AT;
   int64_t rt = op == 2 ? p.E * ((om + AT - 1) / AT) : p.M / AT + (p.E < p.M ? p.E : p.M);
