@@ -83,110 +83,7 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte ? byte << 23 : 0x00400000u);
 }
 
-// Any size and alignment: 128 x 128 tiles of four wavefronts, 32 contraction steps at a time, elements
-// loaded one by one and laid contraction-contiguous in LDS.
-constexpr int AT = 128, AK = 32, AP = AK + 8;
-
-template <int OP, bool X8>
-__global__ __launch_bounds__(256) void grouped_any_kernel(GroupedParams p, int64_t col_tiles) {
-  __shared__ uint16_t sa[AT * AP], sb[AT * AP];
-  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-  const int64_t om = OP == 2 ? p.N : p.M, on = OP == 0 ? p.N : p.K;
-  int e;
-  int64_t m0, m1, n0, c0, c1;  // output rows [m0, m1), columns from n0, contraction [c0, c1)
-  if constexpr (OP == 2) {
-    const int64_t row_tiles = (om + AT - 1) / AT;
-    const bool ok = ragged_ok(p.offs, p.E, p.M);
-    if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = ok ? 0 : 1;
-    if (!ok) return;
-    const int64_t t = blockIdx.x;
-    n0 = t % col_tiles * AT;
-    m0 = t / col_tiles % row_tiles * AT;
-    m1 = m0 + AT < om ? m0 + AT : om;
-    e = (int)(t / col_tiles / row_tiles);
-    c0 = p.offs[e];
-    c1 = p.offs[e + 1];
-  } else {
-    const RowTiles rt = count_row_tiles(p.offs, p.E, p.M, AT);
-    if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = rt.ok ? 0 : 1;
-    if (!rt.ok) return;
-    const RowTile r = find_row_tile(rt, p.offs, p.E, AT, (int)(blockIdx.x / col_tiles));
-    if (r.e < 0) return;
-    e = r.e;
-    m0 = r.m0;
-    m1 = r.m1;
-    n0 = blockIdx.x % col_tiles * AT;
-    c0 = 0;
-    c1 = OP == 0 ? p.K : p.N;
-  }
-  const uint16_t* b = OP == 2 ? p.b : p.b + (int64_t)e * p.N * p.K;
-  f32x16 acc[2][2] = {};
-  const int wr = (wid >> 1) * 64, wc = (wid & 1) * 64;
-  for (int64_t k0 = c0; k0 < c1; k0 += AK) {
-    for (int i = tid; i < AT * AK; i += 256) {
-      // consecutive threads walk the operand's contiguous axis
-      const int kk = OP == 2 ? i / AT : i % AK, rr = OP == 2 ? i % AT : i / AK;
-      const int64_t row = m0 + rr, k = k0 + kk;
-      const bool in = row < m1 && k < c1;
-      sa[rr * AP + kk] = in ? (OP == 2 ? p.a[k * p.lda + row] : p.a[row * p.lda + k]) : (uint16_t)0;
-    }
-    for (int i = tid; i < AT * AK; i += 256) {
-      const int kk = OP == 0 ? i % AK : i / AT, rr = OP == 0 ? i / AK : i % AT;
-      const int64_t col = n0 + rr, k = k0 + kk;
-      uint16_t v = 0;
-      if (col < on && k < c1) {
-        if constexpr (OP == 0) {
-          v = b[col * p.K + k];
-        } else if constexpr (X8) {
-          const float f = __builtin_amdgcn_cvt_f32_fp8((int)p.bq[k * p.K + col], 0);
-          v = (uint16_t)bf16_bits(f * e8m0_value(p.bs[k * ((p.K + 31) / 32) + (col >> 5)]));
-        } else {
-          v = OP == 1 ? b[k * p.K + col] : b[k * p.ldb + col];
-        }
-      }
-      sb[rr * AP + kk] = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < AK / 16; ++s) {
-      bf16x8 fa[2], fb[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int o = s * 16 + 8 * (lane >> 5);
-        fa[i] = *reinterpret_cast<const bf16x8*>(&sa[(wr + i * 32 + (lane & 31)) * AP + o]);
-        fb[i] = *reinterpret_cast<const bf16x8*>(&sb[(wc + i * 32 + (lane & 31)) * AP + o]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
-    __syncthreads();
-  }
-  // accumulator: lane l holds column l % 32 and rows 8 (q / 4) + 4 (l / 32) + q % 4 of a 32 x 32 block
-  const int64_t base = OP == 2 ? (int64_t)e * p.N * p.K : 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int64_t row = m0 + wr + i * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3);
-        const int64_t col = n0 + wc + j * 32 + (lane & 31);
-        if (row < m1 && col < on) {
-          const int64_t o = base + row * p.ldc + col;
-          if (p.out_f32) {
-            float* c = reinterpret_cast<float*>(p.c) + o;
-            *c = p.accum ? *c + acc[i][j][q] : acc[i][j][q];
-          } else {
-            reinterpret_cast<uint16_t*>(p.c)[o] = (uint16_t)bf16_bits(acc[i][j][q]);
-          }
-        }
-      }
-}
-
-// ------------------------------------------------------------------ aligned rows: pipelined tiles
+// ------------------------------------------------------------------ pipelined tiles
 
 // Block tile BM x BN, four wavefronts in a 2 x 2 grid, each owning a (BM/2) x (BN/2) tile of 32 x 32
 // matrix-core fragments (256 x 256: all 256 accumulators of a lane in AGPRs, one block per CU).
@@ -208,7 +105,11 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedParams p, int64
 //     column of four rows. Chunk c of row k sits at c ^ 4 (k % 4): the four rows of a read, 32 bytes
 //     each, and the two 16-column halves of a fragment hit eight different 32-byte bank groups.
 //
-// Bounds: the loads are buffer loads against a descriptor that ends at 2 GB from the tile's first
+// Operands whose rows are not 16-byte aligned, and the MXFP8 codes of OP 2, cannot go to LDS as they are:
+// they are fetched into registers two quarters ahead (16 bytes per load, at any alignment; element by
+// element at a ragged end), decoded if they are codes, and written to the same places of the same units.
+//
+// Bounds: the direct loads are buffer loads against a descriptor that ends at 2 GB from the tile's first
 // element; a lane whose row or column does not exist asks for an offset past it and gets zeros in
 // LDS. So ragged segment ends, odd tile ends and the last contraction stage need no other path, rows of
 // another expert are never read, and 64-bit offsets live in the descriptor's base.
@@ -261,6 +162,10 @@ struct Operand {
       }
     }
     k_lane = KC ? ((l & 7) ^ ((l >> 4) & 7)) * 8 : RPL * NLOAD * wid + l / CPR;
+    init_reads(w0, lds);
+  }
+  __device__ __forceinline__ void init_reads(int w0, uint32_t lds) {
+    const int l = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (KC) {
@@ -297,6 +202,89 @@ struct Operand {
   }
 };
 
+// 16 bytes from any address.
+__device__ __forceinline__ u32x4_t load16_any(const void* p) {
+  u32x4_t v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ uint32_t bf16_of_fp8(uint32_t w, bool hi, float scale) {
+  return __builtin_bit_cast(uint32_t, hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true)
+                                         : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
+}
+
+// An operand that passes through registers: BF16 at any alignment, or (X8, contraction-slow) codes with
+// their scales. LDS layout and reads are Operand's.
+template <bool KC, int R, bool X8>
+struct StagedOperand : Operand<KC, R> {
+  using Base = Operand<KC, R>;
+  static constexpr int PER = X8 ? 16 : 8;            // elements per fetch
+  static constexpr int NF = R * 64 / PER / 256;      // fetches per thread and stage
+  static constexpr int PPR = (KC ? 64 : R) / PER;    // fetches per row
+  const uint8_t* src;   // the tile's first element of the stage to fetch next
+  const uint8_t* scl;   // X8: its row's first scale of this tile
+  int64_t ldb, lds_;    // bytes between rows, scales between rows
+  int valid;
+  u32x4_t v[NF];
+  uint32_t sc[X8 ? NF : 1];
+
+  __device__ __forceinline__ void init(const void* origin, const uint8_t* scales, int64_t ld, int64_t ld_scales,
+                                       int valid_, int w0, uint32_t lds) {
+    Base::init_reads(w0, lds);
+    src = reinterpret_cast<const uint8_t*>(origin);
+    scl = scales;
+    ldb = X8 ? ld : 2 * ld;
+    lds_ = ld_scales;
+    valid = valid_;
+  }
+  __device__ __forceinline__ void fetch(int left) {
+#pragma unroll
+    for (int t = 0; t < NF; ++t) {
+      const int id = t * 256 + (int)threadIdx.x, r = id / PPR, c = id % PPR * PER;
+      const int n = min(PER, KC ? (r < valid ? left - c : 0) : (r < left ? valid - c : 0));
+      const uint8_t* p = src + r * ldb + (X8 ? c : 2 * c);
+      v[t] = (u32x4_t){0, 0, 0, 0};
+      if (X8) sc[t] = n > 0 ? scl[r * lds_ + (c >> 5)] : 0u;
+      if (n == PER) {
+        v[t] = load16_any(p);
+      } else if (n > 0) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const uint32_t x = e < n ? (X8 ? (uint32_t)p[e] : (uint32_t) reinterpret_cast<const uint16_t*>(p)[e]) : 0u;
+          if (X8)
+            v[t][e / 4] |= x << (8 * (e % 4));
+          else
+            v[t][e / 2] |= x << (16 * (e % 2));
+        }
+      }
+    }
+    src += KC ? 128 : 64 * ldb;
+    if (X8) scl += 64 * lds_;
+  }
+  __device__ __forceinline__ void put(uint8_t* unit) const {
+#pragma unroll
+    for (int t = 0; t < NF; ++t) {
+      const int id = t * 256 + (int)threadIdx.x, r = id / PPR, c = id % PPR * PER / 8;  // row, 16-byte chunk
+      uint8_t* row = unit + r * (KC ? 128 : R * 2);
+      if constexpr (X8) {
+        const float s = e8m0_value(sc[t]);
+        u32x4_t lo, hi;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          lo[2 * i] = bf16_of_fp8(v[t][i], false, s);
+          lo[2 * i + 1] = bf16_of_fp8(v[t][i], true, s);
+          hi[2 * i] = bf16_of_fp8(v[t][2 + i], false, s);
+          hi[2 * i + 1] = bf16_of_fp8(v[t][2 + i], true, s);
+        }
+        *reinterpret_cast<u32x4_t*>(row + ((c ^ (4 * (r & 3))) << 4)) = lo;
+        *reinterpret_cast<u32x4_t*>(row + (((c + 1) ^ (4 * (r & 3))) << 4)) = hi;
+      } else {
+        *reinterpret_cast<u32x4_t*>(row + ((c ^ (KC ? (r >> 1) & 7 : 4 * (r & 3))) << 4)) = v[t];
+      }
+    }
+  }
+};
+
 template <int BM, int BN>
 struct TileSize {
   static constexpr int FM = BM / 64, FN = BN / 64;
@@ -309,22 +297,41 @@ struct TileSize {
 
 // Output rows [m0, m0 + mr) and columns [n0, n0 + nc) of the tile, contraction length kc; a and b: the
 // operands' first elements of the tile.
-template <int OP, int BM, int BN, bool F32>
-__device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* smem, const uint16_t* a, const uint16_t* b,
-                                             int64_t ldb, int64_t c_base, int mr, int nc, int kc) {
+// 16 bytes past the caches' retention (outputs are not read again by this launch), or to any address.
+template <bool ANY>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  if constexpr (ANY)
+    __builtin_memcpy(p, &v, 16);
+  else
+    store16_nt(p, v);
+}
+
+enum Feed { DIRECT, STAGED, STAGED_CODES };  // how an operand gets to LDS
+
+template <int OP, int BM, int BN, bool F32, Feed FA, Feed FB>
+__device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* smem, const uint16_t* a, const void* b,
+                                             const uint8_t* b_scales, int64_t ldb, int64_t c_base, int mr, int nc,
+                                             int kc) {
   using S = TileSize<BM, BN>;
   constexpr int FM = S::FM, FN = S::FN;
-  using OA = Operand<OP != 2, BM>;
-  using OB = Operand<OP == 0, BN>;
+  using OA = std::conditional_t<FA == DIRECT, Operand<OP != 2, BM>, StagedOperand<OP != 2, BM, false>>;
+  using OB = std::conditional_t<FB == DIRECT, Operand<OP == 0, BN>, StagedOperand<OP == 0, BN, FB == STAGED_CODES>>;
+  constexpr bool SA = FA != DIRECT, SB = FB != DIRECT;
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
   const int wid_u = __builtin_amdgcn_readfirstlane(wid);
   const int wm = wid >> 1, wn = wid & 1;
   const uint32_t lds0 = lds_addr(smem);
   OA oa;
   OB ob;
-  oa.init(a, p.lda, mr, wid, wm * (BM / 2), lds0);
-  ob.init(b, ldb, nc, wid, wn * (BN / 2), lds0);
-  constexpr int NLA = OA::NLOAD, NLB = OB::NLOAD;  // loads of a unit per wavefront
+  if constexpr (SA)
+    oa.init(a, nullptr, p.lda, 0, mr, wm * (BM / 2), lds0);
+  else
+    oa.init(a, p.lda, mr, wid, wm * (BM / 2), lds0);
+  if constexpr (SB)
+    ob.init(b, b_scales, ldb, (p.K + 31) / 32, nc, wn * (BN / 2), lds0);
+  else
+    ob.init(reinterpret_cast<const uint16_t*>(b), ldb, nc, wid, wn * (BN / 2), lds0);
+  constexpr int NLA = SA ? 0 : OA::NLOAD, NLB = SB ? 0 : OB::NLOAD;  // direct loads of a unit per wavefront
   const uint32_t lds_a = lds0 + wid_u * NLA * 1024, lds_b = lds0 + wid_u * NLB * 1024;  // its part of unit 0
   const int KT = (kc + 63) >> 6;
 
@@ -356,10 +363,11 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
       }
 #pragma unroll
       for (int i = L0 + m * NQ / NM; i < L0 + (m + 1) * NQ / NM; ++i) {
-        if (s == 3 || s == 0)
-          ob.load(i, left, ld);
-        else
-          oa.load(i, left, ld);
+        if constexpr (s == 3 || s == 0) {
+          if constexpr (!SB) ob.load(i, left, ld);
+        } else {
+          if constexpr (!SA) oa.load(i, left, ld);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -370,18 +378,30 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   using Q3 = std::integral_constant<int, 3>;
   constexpr uint32_t U = S::UNIT;
 
-  if (KT > 0) {  // A0 B0 A1 and half of B1
+  if (KT > 0) {  // A0 B0 A1 and half of B1; of staged operands A0 and B0 into registers
+    if constexpr (SA) {
+      oa.fetch(kc);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NLA; ++i) oa.load(i, kc, lds_a);
+      for (int i = 0; i < NLA; ++i) oa.load(i, kc, lds_a);
+      oa.advance();
+    }
+    if constexpr (SB) {
+      ob.fetch(kc);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NLB; ++i) ob.load(i, kc, lds_b + U);
-    oa.advance();
-    ob.advance();
+      for (int i = 0; i < NLB; ++i) ob.load(i, kc, lds_b + U);
+      ob.advance();
+    }
+    if constexpr (!SA) {
 #pragma unroll
-    for (int i = 0; i < NLA; ++i) oa.load(i, kc - 64, lds_a + 2 * U);
-    oa.advance();
+      for (int i = 0; i < NLA; ++i) oa.load(i, kc - 64, lds_a + 2 * U);
+      oa.advance();
+    }
+    if constexpr (!SB) {
 #pragma unroll
-    for (int i = 0; i < NLB / 2; ++i) ob.load(i, kc - 64, lds_b + 3 * U);
+      for (int i = 0; i < NLB / 2; ++i) ob.load(i, kc - 64, lds_b + 3 * U);
+    }
   }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -391,27 +411,37 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   if (KT > 0) {
+    if constexpr (SA) oa.put(smem);
+    if constexpr (SB) ob.put(smem + U);
     wait_vmcnt<NLA + NLB / 2>();  // stage 0 has landed
     __syncthreads();
+    if constexpr (SA) oa.fetch(kc - 64);
+    if constexpr (SB) ob.fetch(kc - 64);
 #pragma unroll
     for (int r = 0; r < NR; ++r) read(r, 0, 0, 0, U);
-    uint32_t ua = 0, ub = U;                    // units of stage kt
+    uint32_t ua = 0, ub = U;                          // units of stage kt
     uint32_t pa = lds_b + 3 * U, pb = lds_a + 4 * U;  // where B of stage kt + 1 and A of stage kt + 2 go
     int left = kc - 64;
 #pragma unroll 1
     for (int kt = 0; kt < KT; ++kt) {
+      const uint32_t na = ua >= 3 * U ? ua - 3 * U : ua + 2 * U;  // units of stage kt + 1
+      const uint32_t nb = ub >= 3 * U ? ub - 3 * U : ub + 2 * U;
       quarter(Q0(), ua, ub, left, pa);
-      ob.advance();
+      if constexpr (SA) oa.put(smem + na);
+      if constexpr (SB) ob.put(smem + nb);
+      if constexpr (!SB) ob.advance();
       left -= 64;
       quarter(Q1(), ua, ub, left, pb);
       quarter(Q2(), ua, ub, left, pb);
-      oa.advance();
+      if constexpr (!SA) oa.advance();
       wait_vmcnt<NLA>();  // all but A of stage kt + 2 has landed
-      __syncthreads();   // for every wavefront, and none reads this stage's units any more
+      __syncthreads();    // for every wavefront, and none reads this stage's units any more
+      if constexpr (SA) oa.fetch(left);  // stage kt + 2
+      if constexpr (SB) ob.fetch(left);
       pa = lds_b + ua;
       pb = lds_a + ub;
-      ua = ua >= 3 * U ? ua - 3 * U : ua + 2 * U;
-      ub = ub >= 3 * U ? ub - 3 * U : ub + 2 * U;
+      ua = na;
+      ub = nb;
       quarter(Q3(), ua, ub, left, pa);
     }
     wait_vmcnt<0>();  // no load may still target LDS
@@ -419,6 +449,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   __syncthreads();  // the slots become the epilogue's staging
 
   // Epilogue: the tile goes through LDS so that stores are 16-byte runs along output rows.
+  constexpr bool ANY = SA || FB == STAGED;  // (the launcher stages operands where the output is unaligned too)
   const int r32 = lane & 31, g = lane >> 5;
   if constexpr (!F32) {
     uint16_t* cs = reinterpret_cast<uint16_t*>(smem);
@@ -438,9 +469,14 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
 #pragma unroll 2
     for (int t = tid; t < BM * CPR; t += 256) {
       const int r = t / CPR, c = t % CPR * 8;
-      if (r < mr && c < nc)
-        store16_nt(reinterpret_cast<uint16_t*>(p.c) + c_base + (int64_t)r * p.ldc + c,
-                   *reinterpret_cast<const uint4*>(cs + r * S::PITCH16 + c));
+      if (r < mr && c < nc) {
+        uint16_t* o = reinterpret_cast<uint16_t*>(p.c) + c_base + (int64_t)r * p.ldc + c;
+        if (!ANY || c + 8 <= nc) {
+          store16<ANY>(o, *reinterpret_cast<const uint4*>(cs + r * S::PITCH16 + c));
+        } else {
+          for (int e = 0; c + e < nc; ++e) o[e] = cs[r * S::PITCH16 + c + e];
+        }
+      }
     }
     return;
   }
@@ -468,11 +504,16 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
       if (row < mr && c < nc) {
         float4 v = *reinterpret_cast<const float4*>(cs + r * S::PITCH32 + c);
         float* o = reinterpret_cast<float*>(p.c) + c_base + (int64_t)row * p.ldc + c;
-        if (p.accum) {
-          const float4 u = *reinterpret_cast<const float4*>(o);
-          v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        if (!ANY || c + 4 <= nc) {
+          if (p.accum) {
+            const float4 u = __builtin_bit_cast(float4, load16_any(o));
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+          }
+          store16<ANY>(o, __builtin_bit_cast(uint4, v));
+        } else {
+          const float* s = cs + r * S::PITCH32 + c;
+          for (int e = 0; c + e < nc; ++e) o[e] = p.accum ? o[e] + s[e] : s[e];
         }
-        store16_nt(o, __builtin_bit_cast(uint4, v));
       }
     }
   }
@@ -490,7 +531,7 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
 // Of T tiles on C compute units the last T mod C would leave most of the chip idle for a whole tile's time:
 // they are split into four quarters, or two halves of the rows, where that many fit the chip at once. Their
 // blocks come first (lowest ids). A tile whose expert ends within its first 128 rows runs as a half.
-template <int OP, int BM, int BN, bool F32>
+template <int OP, int BM, int BN, bool F32, Feed F>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_rows_kernel(GroupedParams p, int col_tiles, int ncu) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN>::LDS];
   const RowTiles rt = count_row_tiles(p.offs, p.E, p.M, BM);
@@ -532,23 +573,24 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_rows_kernel(Gr
       if (mr <= 0 || n0 >= on) return;
     }
     if (split == 4) {
-      grouped_tile<OP, 128, 128, F32>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, m0 * p.ldc + n0,
-                                      mr, (int)min(on - n0, (int64_t)128), (int)kc);
+      grouped_tile<OP, 128, 128, F32, F, F>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, nullptr, p.K,
+          m0 * p.ldc + n0, mr, (int)min(on - n0, (int64_t)128), (int)kc);
       return;
     }
     if (mr <= 128) {
-      grouped_tile<OP, 128, 256, F32>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, m0 * p.ldc + n0,
-                                      mr, (int)min(on - n0, (int64_t)256), (int)kc);
+      grouped_tile<OP, 128, 256, F32, F, F>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, nullptr, p.K,
+          m0 * p.ldc + n0, mr, (int)min(on - n0, (int64_t)256), (int)kc);
       return;
     }
   }
-  grouped_tile<OP, BM, BN, F32>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, p.K, m0 * p.ldc + n0, mr,
+  grouped_tile<OP, BM, BN, F32, F, F>(p, smem, p.a + m0 * p.lda, OP == 0 ? w + n0 * p.K : w + n0, nullptr, p.K,
+          m0 * p.ldc + n0, mr,
                                 (int)min(on - n0, (int64_t)BN), (int)kc);
 }
 
 // OP 2: one grid of output tiles per expert, experts with the most rows first (their blocks run longest),
 // in index order past 64 experts.
-template <int BM, int BN, bool F32>
+template <int BM, int BN, bool F32, Feed FA, Feed FB>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_dw_kernel(GroupedParams p, int row_tiles, int col_tiles) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN>::LDS];
   const bool ok = ragged_ok(p.offs, p.E, p.M);
@@ -576,9 +618,17 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_dw_kernel(Grou
   const uint32_t rows = min(GM, (uint32_t)row_tiles - grp * GM);
   const int64_t m0 = (int64_t)(grp * GM + in % rows) * BM, n0 = (int64_t)(in / rows) * BN;
   if (p.accum && c1 == c0) return;  // nothing to add
-  grouped_tile<2, BM, BN, F32>(p, smem, p.a + (int64_t)c0 * p.lda + m0, p.b + (int64_t)c0 * p.ldb + n0, p.ldb,
-                          (int64_t)e * p.N * p.K + m0 * p.ldc + n0, (int)min(p.N - m0, (int64_t)BM),
-                          (int)min(p.K - n0, (int64_t)BN), c1 - c0);
+  const void* b = p.b + (int64_t)c0 * p.ldb + n0;
+  const uint8_t* scales = nullptr;
+  int64_t ldb = p.ldb;
+  if constexpr (FB == STAGED_CODES) {
+    b = p.bq + (int64_t)c0 * p.K + n0;
+    scales = p.bs + (int64_t)c0 * ((p.K + 31) / 32) + (n0 >> 5);
+    ldb = p.K;
+  }
+  grouped_tile<2, BM, BN, F32, FA, FB>(p, smem, p.a + (int64_t)c0 * p.lda + m0, b, scales, ldb,
+                                       (int64_t)e * p.N * p.K + m0 * p.ldc + n0, (int)min(p.N - m0, (int64_t)BM),
+                                       (int)min(p.K - n0, (int64_t)BN), c1 - c0);
 }
 
 }  // namespace mxf
@@ -587,25 +637,28 @@ namespace {
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int OP, int BM, int BN, bool F32>
+template <int OP, int B, bool F32, mxf::Feed FA, mxf::Feed FB>
 hipError_t launch_tiles_as(const mxf::GroupedParams& p, int ncu, hipStream_t st) {
-  const int64_t on = OP == 0 ? p.N : p.K, ct = (on + BN - 1) / BN;
+  const int64_t on = OP == 0 ? p.N : p.K, ct = (on + B - 1) / B;
   if constexpr (OP == 2) {
-    const int64_t rt = (p.N + BM - 1) / BM;
-    hipLaunchKernelGGL((mxf::grouped_dw_kernel<BM, BN, F32>), dim3((unsigned)(p.E * rt * ct)), dim3(256), 0, st, p, (int)rt,
-                       (int)ct);
+    const int64_t rt = (p.N + B - 1) / B;
+    hipLaunchKernelGGL((mxf::grouped_dw_kernel<B, B, F32, FA, FB>), dim3((unsigned)(p.E * rt * ct)), dim3(256), 0, st, p,
+                       (int)rt, (int)ct);
   } else {
-    int64_t rt = p.M / BM + (p.E < p.M ? p.E : p.M);  // every expert may end inside a tile
-    if (rt == 0) rt = 1;                              // (one block looks at the offsets)
-    hipLaunchKernelGGL((mxf::grouped_rows_kernel<OP, BM, BN, F32>), dim3((unsigned)(rt * ct + (BM == 256 ? ncu : 0))), dim3(256), 0,
-                       st, p, (int)ct, ncu);  // (+ ncu: the blocks of split tiles)
-  }
+    int64_t rt = p.M / B + (p.E < p.M ? p.E : p.M);  // every expert may end inside a tile
+    if (rt == 0) rt = 1;                             // (one block looks at the offsets)
+    hipLaunchKernelGGL((mxf::grouped_rows_kernel<OP, B, B, F32, FA>),
+                       dim3((unsigned)(rt * ct + (B == 256 ? ncu + 8 : 0))), dim3(256), 0, st, p, (int)ct, ncu);
+  }  // (ncu + 8 more: the blocks of split tiles)
   return hipGetLastError();
 }
-
-template <int OP, int BM, int BN>
-hipError_t launch_tiles(const mxf::GroupedParams& p, int ncu, hipStream_t st) {
-  return p.out_f32 ? launch_tiles_as<OP, BM, BN, true>(p, ncu, st) : launch_tiles_as<OP, BM, BN, false>(p, ncu, st);
+template <int OP, mxf::Feed FA, mxf::Feed FB>
+hipError_t launch_tiles(const mxf::GroupedParams& p, bool big, int ncu, hipStream_t st) {
+  if (big)
+    return p.out_f32 ? launch_tiles_as<OP, 256, true, FA, FB>(p, ncu, st)
+                     : launch_tiles_as<OP, 256, false, FA, FB>(p, ncu, st);
+  return p.out_f32 ? launch_tiles_as<OP, 128, true, FA, FB>(p, ncu, st)
+                   : launch_tiles_as<OP, 128, false, FA, FB>(p, ncu, st);
 }
 
 }  // namespace
@@ -614,28 +667,17 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
   using namespace mxf;
   const int64_t om = op == 2 ? p.N : p.M, on = op == 0 ? p.N : p.K;
   // 16-byte rows, and offsets inside a tile that a descriptor covers (256 rows of ld elements < 2 GB)
-  const bool aligned = p.N % 8 == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && p.ldb % 8 == 0 &&
+  const bool aligned = p.N % 8 == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && (p.bq || p.ldb % 8 == 0) &&
                        p.ldc % (p.out_f32 ? 4 : 8) == 0 && a16(p.a) && a16(p.b) && a16(p.c) && p.lda < (1 << 22) &&
-                       p.ldb < (1 << 22) && !p.bq;
-  if (aligned) {
-    // 256 x 256 tiles where they fill the chip
-    const int64_t big = (op == 2 ? p.E * ((om + 255) / 256) : (om + 255) / 256) * ((on + 255) / 256);
-    const bool b256 = big >= ncu;
-    if (op == 0) return b256 ? launch_tiles<0, 256, 256>(p, ncu, st) : launch_tiles<0, 128, 128>(p, ncu, st);
-    if (op == 1) return b256 ? launch_tiles<1, 256, 256>(p, ncu, st) : launch_tiles<1, 128, 128>(p, ncu, st);
-    return b256 ? launch_tiles<2, 256, 256>(p, ncu, st) : launch_tiles<2, 128, 128>(p, ncu, st);
-  }
-  const int64_t ct = (on + AT - 1) / AT;
-  int64_t rt = op == 2 ? p.E * ((om + AT - 1) / AT) : p.M / AT + (p.E < p.M ? p.E : p.M);
-  if (rt == 0) rt = 1;
-  const dim3 g((unsigned)(rt * ct)), b(256);
+                       p.ldb < (1 << 22);
+  // 256 x 256 tiles where they fill the chip
+  const bool big = (op == 2 ? p.E * ((om + 255) / 256) : (om + 255) / 256) * ((on + 255) / 256) >= ncu;
   if (op == 0)
-    hipLaunchKernelGGL((grouped_any_kernel<0, false>), g, b, 0, st, p, ct);
-  else if (op == 1)
-    hipLaunchKernelGGL((grouped_any_kernel<1, false>), g, b, 0, st, p, ct);
-  else if (p.bq)
-    hipLaunchKernelGGL((grouped_any_kernel<2, true>), g, b, 0, st, p, ct);
-  else
-    hipLaunchKernelGGL((grouped_any_kernel<2, false>), g, b, 0, st, p, ct);
-  return hipGetLastError();
+    return aligned ? launch_tiles<0, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<0, STAGED, STAGED>(p, big, ncu, st);
+  if (op == 1)
+    return aligned ? launch_tiles<1, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<1, STAGED, STAGED>(p, big, ncu, st);
+  if (p.bq)
+    return aligned ? launch_tiles<2, DIRECT, STAGED_CODES>(p, big, ncu, st)
+                   : launch_tiles<2, STAGED, STAGED_CODES>(p, big, ncu, st);
+  return aligned ? launch_tiles<2, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<2, STAGED, STAGED>(p, big, ncu, st);
 }

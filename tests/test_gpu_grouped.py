@@ -89,6 +89,67 @@ def test_larger_products(counts, N, K):
     check_all(counts, N, K, 77)
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([5000, 0, 3000, 130, 3900, 1], 2816, 192),  # 550 tiles of 256 x 256: the last 38 run as quarters
+    ([9000], 2560, 136),                         # 360: the last 104 as halves
+    ([4000, 100, 257, 4643], 2560, 64),          # 370: no split; an expert that ends in a tile's first half
+    ([5000, 0, 3000, 130, 3900, 1], 2811, 197),  # the same, rows of any alignment
+    ([9000], 2555, 131)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_large_tiles(counts, N, K, out):
+    """Row counts that fill the chip with the largest tiles, in the forward and (N, K exchanged) the input
+    gradient."""
+    mx = require_gpu()
+    offs, toffs, x, w, dy = problem(counts, N, K, N)
+    (y, _, _), (my, _, _) = reference(x, w, dy, offs)
+    close(mx.grouped_gemm_fwd(x, w, toffs, out_dtype=out), y, my, K, "fwd")
+    del y, my
+    offs, toffs, x, w, dy = problem(counts, K, N, N + 1)
+    (_, dx, _), (_, mdx, _) = reference(x, w, dy, offs)
+    close(mx.grouped_gemm_dgrad(dy, w, toffs, out_dtype=out), dx, mdx, K, "dgrad")
+
+
+@pytest.mark.parametrize("counts,N,K", [([100, 0, 333, 64, 1, 70], 1500, 2000), ([100, 0, 333, 64, 1, 70], 1501, 1999),
+                                        ([65] * 5 + [0] * 63, 400, 504)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_large_weight_gradients(counts, N, K, out):
+    """More output tiles than compute units, from BF16 rows and from codes; and more than 64 experts."""
+    mx = require_gpu()
+    offs, toffs, x, w, dy = problem(counts, N, K, 5)
+    (_, _, dw), (_, _, mdw) = reference(x, w, dy, offs)
+    close(mx.grouped_gemm_wgrad(dy, x, toffs, out_dtype=out), dw, mdw, max(counts), "wgrad")
+    q, s = ob.mx_rows(f64(x))
+    xd = torch.from_numpy(ob.mx_values(q, s)).cuda()
+    (_, _, dw), (_, _, mdw) = reference(xd, w, dy, offs)
+    q, s = torch.from_numpy(np.ascontiguousarray(q)).cuda(), torch.from_numpy(s).cuda()
+    close(mx.grouped_gemm_wgrad(dy, (q, s), toffs, out_dtype=out), dw, mdw, max(counts), "wgrad of codes")
+
+
+@pytest.mark.parametrize("N,K", [(64, 512), (63, 257)])
+def test_every_code_and_scale_enters_the_product_unrounded(N, K):
+    """dy = the identity: dw[n, k] is the decoded x[n, k] itself. Scales that keep a code's value a normal BF16
+    number (from 2^-117: the smallest code is 2^-9)."""
+    mx = require_gpu()
+    r = np.random.default_rng(1)
+    q = r.integers(0, 256, size=(N, K)).astype(np.uint8)
+    q[(q & 0x7F) == 0x7F] = 0  # NaN codes: below
+    s = r.integers(10, 246, size=(N, -(-K // 32))).astype(np.uint8)
+    dy = torch.eye(N, dtype=torch.bfloat16, device="cuda")
+    offs = torch.tensor([0, N], dtype=torch.int32, device="cuda")
+    tq, ts = torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()
+    got = mx.grouped_gemm_wgrad(dy, (tq, ts), offs, out_dtype=torch.float32)
+    assert np.array_equal(f64(got)[0], ob.mx_values(q, s))
+    # a NaN scale and a NaN code: NaN in the columns of its group (0 x NaN), in its column, in no other
+    ts[5, 2] = 255
+    tq[9, 40] = 0x7F
+    tq[5, 64:96] = 0x12
+    bad = mx.grouped_gemm_wgrad(dy, (tq, ts), offs, out_dtype=torch.float32)[0].isnan()
+    want = torch.zeros_like(bad)
+    want[:, 64:96] = True
+    want[:, 40] = True
+    assert torch.equal(bad, want)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 33, 64, 65, 100])
 def test_few_rows_in_one_expert_of_many(rows):
     """Serving: a handful of rows, all in one expert or one each."""
