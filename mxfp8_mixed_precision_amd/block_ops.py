@@ -23,36 +23,40 @@ def _t():
     return _torch
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _bad(what):
+    raise ValueError(what)
 
 
 def _rows(t, name):
     """A matrix with adjacent columns as (rows, cols, row stride)."""
-    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), f"{name}: a 2-D tensor with adjacent columns is needed")
+    if not (t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1)):
+        _bad(f"{name}: a 2-D tensor with adjacent columns is needed")
     rows, cols = t.shape
     ld = t.stride(0) if rows > 1 else cols
-    _need(ld >= cols, f"{name}: rows overlap (stride {ld} < {cols})")
+    if not (ld >= cols):
+        _bad(f"{name}: rows overlap (stride {ld} < {cols})")
     return rows, cols, ld
 
 
 def _on(t, device, name):
-    _need(t.device == device, f"{name} is on {t.device}, not on {device}")
+    if not (t.device == device):
+        _bad(f"{name} is on {t.device}, not on {device}")
 
 
 def _dense(t, shape, dtype, device, name):
-    _need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(),
-          f"{name}: a dense {dtype} tensor of shape {shape} is needed")
+    if not (t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()):
+        _bad(f"{name}: a dense {dtype} tensor of shape {shape} is needed")
     _on(t, device, name)
 
 
 def _stream_of(device):
     """The current stream of the tensors' device, which has to be the current device."""
-    cuda = _t().cuda
-    _need(device.type == "cuda", f"tensors on {device}: a GPU is needed")
-    _need(device.index == cuda.current_device(), f"tensors are on {device}, not on the current device")
-    return cuda.current_stream().cuda_stream
+    if device.type != "cuda":
+        _bad(f"tensors on {device}: a GPU is needed")
+    torch = _t()
+    if device.index != torch.cuda.current_device():
+        _bad(f"tensors are on {device}, not on the current device")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _on_stream(fn):
@@ -71,16 +75,19 @@ def _on_stream(fn):
 
 def _norm_args(x, weight, bias):
     torch = _t()
-    _need(x.dtype in (torch.bfloat16, torch.float32), f"element type {x.dtype}: bfloat16 or float32 is needed")
+    if not (x.dtype in (torch.bfloat16, torch.float32)):
+        _bad(f"element type {x.dtype}: bfloat16 or float32 is needed")
     flags = _abi.NORM_F32 if x.dtype == torch.float32 else 0
     cols = x.shape[-1]
     for name, v in (("weight", weight), ("bias", bias)):
         if v is not None:
-            _need(v.dtype in (torch.bfloat16, torch.float32), f"{name}: bfloat16 or float32 is needed")
+            if not (v.dtype in (torch.bfloat16, torch.float32)):
+                _bad(f"{name}: bfloat16 or float32 is needed")
             _dense(v, (cols,), v.dtype, x.device, name)
             if v.dtype == torch.float32:
                 flags |= _abi.NORM_WEIGHT_F32
-    _need(weight is None or bias is None or weight.dtype == bias.dtype, "weight and bias differ in type")
+    if not (weight is None or bias is None or weight.dtype == bias.dtype):
+        _bad("weight and bias differ in type")
     return flags
 
 
@@ -122,7 +129,8 @@ def _norm_bwd(dy, x, q, s, mean, rstd, weight):
     dev = dy.device
     ldx = cols
     if x is not None:
-        _need(x.dtype == dy.dtype and tuple(x.shape) == (rows, cols), "x and dy differ in type or shape")
+        if not (x.dtype == dy.dtype and tuple(x.shape) == (rows, cols)):
+            _bad("x and dy differ in type or shape")
         _on(x, dev, "x")
         ldx = _rows(x, "x")[2]
         _dense(mean, (rows,), torch.float32, dev, "mean")
@@ -157,9 +165,11 @@ def swiglu_ckpt_fwd(gu):
     """h = BF16(g sigmoid(g) u) of gu [rows, 2F] BF16 (gate | up), and gu in 8 bits: (h, q, s) with q
     [2 rows, F] and s [2 rows, ceil(F / 32)]."""
     torch = _t()
-    _need(gu.dtype == torch.bfloat16, "gu: bfloat16 is needed")
+    if not (gu.dtype == torch.bfloat16):
+        _bad("gu: bfloat16 is needed")
     rows, cols, ld = _rows(gu, "gu")
-    _need(cols % 2 == 0, f"gu: an even number of columns is needed, not {cols}")
+    if not (cols % 2 == 0):
+        _bad(f"gu: an even number of columns is needed, not {cols}")
     F, dev = cols // 2, gu.device
     h = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
     q = torch.empty((2 * rows, F), dtype=torch.uint8, device=dev)
@@ -173,7 +183,8 @@ def swiglu_ckpt_bwd(dh, q, s, recompute=True):
     """(dgu, h) of swiglu_ckpt_fwd from its checkpoint: dgu [rows, 2F], and the activation h again (None
     with recompute=False)."""
     torch = _t()
-    _need(dh.dtype == torch.bfloat16, "dh: bfloat16 is needed")
+    if not (dh.dtype == torch.bfloat16):
+        _bad("dh: bfloat16 is needed")
     rows, F, ld = _rows(dh, "dh")
     dev = dh.device
     _dense(q, (2 * rows, F), torch.uint8, dev, "q")
@@ -191,9 +202,11 @@ def _grouped_args(w_shape, offs, device, out_dtype, status):
     E = w_shape[0]
     _dense(offs, (E + 1,), torch.int32, device, "offs")
     if status is not None:
-        _need(status.dtype == torch.int32 and status.numel() >= 1, "status: an int32 tensor is needed")
+        if not (status.dtype == torch.int32 and status.numel() >= 1):
+            _bad("status: an int32 tensor is needed")
         _on(status, device, "status")
-    _need(out_dtype in (torch.bfloat16, torch.float32), f"out_dtype {out_dtype}: bfloat16 or float32 is needed")
+    if not (out_dtype in (torch.bfloat16, torch.float32)):
+        _bad(f"out_dtype {out_dtype}: bfloat16 or float32 is needed")
     return _abi.GROUPED_OUT_F32 if out_dtype == torch.float32 else 0
 
 
@@ -203,9 +216,11 @@ def grouped_gemm_fwd(x, w, offs, out_dtype=None, status=None):
     offs[E] are left as allocated."""
     torch = _t()
     out_dtype = out_dtype or torch.bfloat16
-    _need(x.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.dim() == 3, "x and w [E, N, K]: bfloat16 is needed")
+    if not (x.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.dim() == 3):
+        _bad("x and w [E, N, K]: bfloat16 is needed")
     M, K, ld = _rows(x, "x")
-    _need(w.shape[2] == K and w.is_contiguous(), f"w: a dense [E, N, {K}] tensor is needed")
+    if not (w.shape[2] == K and w.is_contiguous()):
+        _bad(f"w: a dense [E, N, {K}] tensor is needed")
     _on(w, x.device, "w")
     flags = _grouped_args(w.shape, offs, x.device, out_dtype, status)
     E, N, _ = w.shape
@@ -220,9 +235,11 @@ def grouped_gemm_dgrad(dy, w, offs, out_dtype=None, status=None):
     """dx [M, K]: rows [offs[e], offs[e+1]) of dy [M, N] times w[e] [N, K]."""
     torch = _t()
     out_dtype = out_dtype or torch.bfloat16
-    _need(dy.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.dim() == 3, "dy and w [E, N, K]: bfloat16 is needed")
+    if not (dy.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.dim() == 3):
+        _bad("dy and w [E, N, K]: bfloat16 is needed")
     M, N, ld = _rows(dy, "dy")
-    _need(w.shape[1] == N and w.is_contiguous(), f"w: a dense [E, {N}, K] tensor is needed")
+    if not (w.shape[1] == N and w.is_contiguous()):
+        _bad(f"w: a dense [E, {N}, K] tensor is needed")
     _on(w, dy.device, "w")
     flags = _grouped_args(w.shape, offs, dy.device, out_dtype, status)
     E, _, K = w.shape
@@ -238,24 +255,29 @@ def grouped_gemm_wgrad(dy, x, offs, out_dtype=None, accumulate=None, status=None
     x is BF16, or a pair (q, s): its row-wise MXFP8 codes [M, K] and scales [M, ceil(K / 32)].
     accumulate: an FP32 [E, N, K] tensor that the gradient is added to and that is returned."""
     torch = _t()
-    _need(dy.dtype == torch.bfloat16, "dy: bfloat16 is needed")
+    if not (dy.dtype == torch.bfloat16):
+        _bad("dy: bfloat16 is needed")
     M, N, ldy = _rows(dy, "dy")
     q = s = None
     if isinstance(x, (tuple, list)):
         q, s = x
         x = None
-        _need(q.dim() == 2, "q: a 2-D tensor is needed")
+        if not (q.dim() == 2):
+            _bad("q: a 2-D tensor is needed")
         K = ldx = q.shape[1]
         _dense(q, (M, K), torch.uint8, dy.device, "q")
         _dense(s, (M, (K + 31) // 32), torch.uint8, dy.device, "s")
     else:
-        _need(x.dtype == torch.bfloat16, "x: bfloat16 is needed")
+        if not (x.dtype == torch.bfloat16):
+            _bad("x: bfloat16 is needed")
         rows, K, ldx = _rows(x, "x")
-        _need(rows == M, f"x has {rows} rows, dy {M}")
+        if not (rows == M):
+            _bad(f"x has {rows} rows, dy {M}")
         _on(x, dy.device, "x")
     E = offs.numel() - 1
     if accumulate is not None:
-        _need(out_dtype in (None, torch.float32), "accumulate: the output is float32")
+        if not (out_dtype in (None, torch.float32)):
+            _bad("accumulate: the output is float32")
         _dense(accumulate, (E, N, K), torch.float32, dy.device, "accumulate")
         out_dtype, dw = torch.float32, accumulate
     else:

@@ -8,9 +8,11 @@
 // Bound: HBM. A row is read once and stays in registers as FP32 while its two sums are formed, so
 // the variance is the second, centred pass over the same registers (no cancellation of
 // sum x^2 - mean^2) at no memory cost. TPR threads share a row (a wavefront, or a block with one
-// LDS exchange per sum) and NE elements of it live in each thread; the column a register holds
-// is fixed, so a block that walks rows keeps w and b (and in the backward its share of dw and db)
-// in registers for all of them.
+// LDS exchange per sum) and NE elements of it live in each thread, in chunks of 16 bytes; the column a
+// register holds is fixed, so a block that walks rows keeps w and b (and in the backward its share of
+// dw and db) in registers for all of them. The next row's loads are issued before this row's sums are
+// formed: without them a block waits out a full memory latency per row. Chunks are loaded and stored
+// whole at any alignment; only the chunk in which a row ends goes element by element.
 //
 // The backward's column sums have no atomics: block p leaves one partial row of dw and of db in the
 // workspace and a second launch adds the partial rows in index order, so equal inputs give equal
@@ -30,38 +32,79 @@ template <class T>
 struct Elem;
 template <>
 struct Elem<uint16_t> {  // BF16 bit patterns
+  static constexpr int VEC = 8;
   static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
   static __device__ __forceinline__ uint16_t put(float f) { return (uint16_t)bf16_bits(f); }
+  static __device__ __forceinline__ void unpack(u32x4_t v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(v[i]);
+      f[2 * i + 1] = bf16_hi(v[i]);
+    }
+  }
+  static __device__ __forceinline__ u32x4_t pack(const float* f) {
+    return (u32x4_t){bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7])};
+  }
 };
 template <>
 struct Elem<float> {
+  static constexpr int VEC = 4;
   static __device__ __forceinline__ float get(float v) { return v; }
   static __device__ __forceinline__ float put(float f) { return f; }
+  static __device__ __forceinline__ void unpack(u32x4_t v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  }
+  static __device__ __forceinline__ u32x4_t pack(const float* f) {
+    return (u32x4_t){__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  }
 };
 
-// VEC consecutive elements (16 bytes, or one element) as FP32.
-template <class T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float* f) {
-  if constexpr (VEC == 1) {
-    f[0] = Elem<T>::get(*p);
-  } else if constexpr (VEC == 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
-  } else {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+// N elements at p as FP32, of which the first n exist (n >= N: all); the others are zero.
+template <class T, int N>
+struct Chunk {
+  static constexpr int B = N * (int)sizeof(T), W = (B + 15) / 16;
+  u32x4_t v[W];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if (n >= N) {
+      if constexpr (B >= 16) {
+        __builtin_memcpy(v, p, B);
+      } else {
+        v[0] = (u32x4_t){0, 0, 0, 0};
+        __builtin_memcpy(v, p, B);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = (u32x4_t){0, 0, 0, 0};
+    if (n <= 0) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 4)
+          v[i / 4][i % 4] = __builtin_bit_cast(uint32_t, p[i]);
+        else
+          v[i / 8][i % 8 / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+      }
   }
-}
-template <class T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float* f) {
-  if constexpr (VEC == 1) {
-    *p = Elem<T>::put(f[0]);
-  } else if constexpr (VEC == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]),
-                                              bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7]));
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(v[i / 4][i % 4]);
+    else
+      return i % 2 ? bf16_hi(v[i / 8][i % 8 / 2]) : bf16_lo(v[i / 8][i % 8 / 2]);
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void store_chunk(T* p, const float* f, int n) {
+  constexpr int VEC = Elem<T>::VEC;
+  if (n >= VEC) {
+    const u32x4_t v = Elem<T>::pack(f);
+    __builtin_memcpy(p, &v, 16);
   } else {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i < n) p[i] = Elem<T>::put(f[i]);
   }
 }
 
@@ -77,32 +120,42 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// Sum of a pair over the TPR threads of a row. TPR 64 is one wavefront; more is the whole block, with
-// one barrier: the slots alternate, so the next call's writes cannot meet this call's reads.
-template <int TPR>
+// Sum of a pair over the TPR threads of a row; a block of BLK threads holds BLK / TPR rows. TPR 64 is one
+// wavefront; more takes one barrier of the block: the slots alternate, so the next call's writes
+// cannot meet this call's reads. `red`: 2 * BLK / 64 slots.
+template <int TPR, int BLK>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float2* red, int& phase) {
   a = wave_sum(a);
   b = wave_sum(b);
   if constexpr (TPR > 64) {
-    constexpr int NW = TPR / 64;
-    float2* slot = red + phase * NW;
+    float2* slot = red + phase * (BLK / 64);
     phase ^= 1;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = make_float2(a, b);
     __syncthreads();
+    slot += threadIdx.x / TPR * (TPR / 64);
     a = 0.0f;
     b = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
+    for (int i = 0; i < TPR / 64; ++i) {
       const float2 v = slot[i];
       a += v.x;
       b += v.y;
     }
   }
 }
-template <int TPR>
+template <int TPR, int BLK>
 __device__ __forceinline__ float row_sum(float a, float2* red, int& phase) {
-  float b = 0.0f;
-  row_sum2<TPR>(a, b, red, phase);
+  a = wave_sum(a);
+  if constexpr (TPR > 64) {
+    float2* slot = red + phase * (BLK / 64);
+    phase ^= 1;
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6].x = a;
+    __syncthreads();
+    slot += threadIdx.x / TPR * (TPR / 64);
+    a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) a += slot[i].x;
+  }
   return a;
 }
 
@@ -120,18 +173,18 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
   return m;
 }
 
-// Quantize VEC normalised values (zeros where the lane is past the row's end) and store codes and
-// the group's scale. `on`: the lane's elements exist. Every lane of the group calls this.
+// Quantize VEC normalised values, of which the first n exist (the others are zero), and store codes and the
+// group's scale at column c. Every lane of the group calls this.
 template <int VEC>
-__device__ __forceinline__ void put_codes(const float* xh, bool on, int64_t c, uint8_t* q, uint8_t* s) {
+__device__ __forceinline__ void put_codes(const float* xh, int n, int c, uint8_t* q, uint8_t* s) {
   if constexpr (VEC == 1) {
     const uint32_t v = bf16_bits(xh[0]);
     const Scale sc = scale_from_amax(group_max<1>(v & 0x7FFFu));
     const uint32_t code = cvt2<false>(0u, v, sc) | sc.nanmask;
-    if (on) q[c] = (uint8_t)code;
-    if (on && (c & 31) == 0) s[c >> 5] = (uint8_t)sc.byte;
+    if (n > 0) q[c] = (uint8_t)code;
+    if (n > 0 && (c & 31) == 0) s[c >> 5] = (uint8_t)sc.byte;
   } else {
-    uint32_t w[VEC / 2];
+    uint32_t w[VEC / 2], k[VEC / 4];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) {
@@ -139,112 +192,109 @@ __device__ __forceinline__ void put_codes(const float* xh, bool on, int64_t c, u
       m = pk_max_u16(m, mag2(w[i]));
     }
     const Scale sc = scale_from_amax(group_max<VEC>(max(m & 0xFFFFu, m >> 16)));
-    if (on) {
-      if constexpr (VEC == 8)
-        *reinterpret_cast<uint2*>(q + c) = make_uint2(cvt4(w[0], w[1], sc), cvt4(w[2], w[3], sc));
-      else
-        *reinterpret_cast<uint32_t*>(q + c) = cvt4(w[0], w[1], sc);
-      if ((c & 31) == 0) s[c >> 5] = (uint8_t)sc.byte;
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) k[i] = cvt4(w[2 * i], w[2 * i + 1], sc);
+    if (n >= VEC) {
+      __builtin_memcpy(q + c, k, VEC);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (i < n) q[c + i] = (uint8_t)(k[i / 4] >> (8 * (i % 4)));
     }
+    if (n > 0 && (c & 31) == 0) s[c >> 5] = (uint8_t)sc.byte;
   }
 }
 
-// VEC checkpointed values decoded to FP32 (exact: a code has four significant bits).
-template <int VEC>
-__device__ __forceinline__ void get_codes(const uint8_t* q, const uint8_t* s, int64_t c, float* xh) {
-  const uint32_t byte = s[c >> 5];
-  const float sc = byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte ? byte << 23 : 0x00400000u);
-  if constexpr (VEC == 1) {
-    xh[0] = __builtin_amdgcn_cvt_f32_fp8((int)q[c], 0) * sc;
-  } else {
-    uint32_t w[2];
-    if constexpr (VEC == 8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(q + c);
-      w[0] = v.x;
-      w[1] = v.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(q + c);
-    }
-#pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-      xh[4 * i + 0] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 0) * sc;
-      xh[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 1) * sc;
-      xh[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 2) * sc;
-      xh[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 3) * sc;
-    }
-  }
+// The E8M0 scale's value, and a code word's four decoded values (exact: a code has four significant bits).
+__device__ __forceinline__ float ckpt_scale(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+__device__ __forceinline__ float ckpt_value(const uint32_t* k, int i, float sc) {
+  const int w = (int)k[i / 4];
+  const float f = i % 4 == 0   ? __builtin_amdgcn_cvt_f32_fp8(w, 0)
+                  : i % 4 == 1 ? __builtin_amdgcn_cvt_f32_fp8(w, 1)
+                  : i % 4 == 2 ? __builtin_amdgcn_cvt_f32_fp8(w, 2)
+                               : __builtin_amdgcn_cvt_f32_fp8(w, 3);
+  return f * sc;
 }
 
 // ------------------------------------------------------------------ forward
 
-template <class T, int VEC, int TPR, int NE>
+template <class T, class W, int TPR, int NE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormParams p) {
-  constexpr int BLK = TPR > 256 ? TPR : 256;
-  constexpr int RPB = BLK / TPR;  // rows in flight per block
-  constexpr int NC = NE / VEC;    // chunks per thread
-  static_assert(TPR == 64 || TPR == BLK, "a row belongs to one wavefront or to the whole block");
-  __shared__ float2 red[TPR > 64 ? 2 * (TPR / 64) : 1];
+  constexpr int BLK = TPR > 256 ? TPR : 256, RPB = BLK / TPR;  // rows in flight per block
+  static_assert(TPR == 64 || RPB == 1, "rows of several wavefronts have a block of their own");
+  constexpr int VEC = Elem<T>::VEC, NC = NE / VEC;             // chunks per thread
+  __shared__ float2 red[2 * (BLK / 64)];
   int phase = 0;
-  const int t = threadIdx.x % TPR;
-  const float n = (float)p.cols;  // divided by, so that a constant row's mean is exact
-  float w[NE], b[NE];
+  const int t = threadIdx.x % TPR, cols = (int)p.cols;
+  const float n = (float)cols;  // divided by, so that a constant row's mean is exact
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  Chunk<T, VEC> x[NC];
+  Chunk<W, VEC> w[NC], b[NC];
+  auto fetch = [&](int64_t r) {
+    const T* src = reinterpret_cast<const T*>(p.x) + r * p.ldx;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      x[j].load(src + c, cols - c);
+    }
+  };
+  if (row < p.rows) fetch(row);
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int64_t c = (int64_t)(j * TPR + t) * VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const bool in = c < p.cols;
-      w[j * VEC + i] = in ? weight_at(p.w, p.w_f32, c + i, 1.0f) : 0.0f;
-      b[j * VEC + i] = in ? weight_at(p.b, p.w_f32, c + i, 0.0f) : 0.0f;
-    }
+    const int c = (j * TPR + t) * VEC;
+    if (p.w) w[j].load(reinterpret_cast<const W*>(p.w) + c, cols - c);
+    if (p.b) b[j].load(reinterpret_cast<const W*>(p.b) + c, cols - c);
   }
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < p.rows; row += (int64_t)gridDim.x * RPB) {
-    const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx;
-    T* y = reinterpret_cast<T*>(p.y) + row * p.ldy;
+  const int G = (cols + 31) >> 5;
+  for (; row < p.rows; row += step) {
     float v[NE];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int64_t c = (int64_t)(j * TPR + t) * VEC;
-      if (c < p.cols) {
-        load_vec<T, VEC>(x + c, v + j * VEC);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[j * VEC + i] = 0.0f;
-      }
+      Elem<T>::unpack(x[j].v[0], v + j * VEC);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) sum += v[j * VEC + i];
     }
-    const float mean = row_sum<TPR>(sum, red, phase) / n;
+    if (row + step < p.rows) fetch(row + step);
+    const float mean = row_sum<TPR, BLK>(sum, red, phase) / n;
     float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const bool in = (int64_t)(j * TPR + t) * VEC < p.cols;
+      const int m = cols - (j * TPR + t) * VEC;
+      const bool whole = (j + 1) * TPR * VEC <= cols;  // for every lane
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        v[j * VEC + i] = in ? v[j * VEC + i] - mean : 0.0f;
-        ss += v[j * VEC + i] * v[j * VEC + i];
+        float& d = v[j * VEC + i];
+        d = whole || i < m ? d - mean : 0.0f;
+        ss += d * d;
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(ss, red, phase) / n + p.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<TPR, BLK>(ss, red, phase) / n + p.eps);
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
     }
+    T* y = reinterpret_cast<T*>(p.y) + row * p.ldy;
+    uint8_t* q = p.q + row * cols;
+    uint8_t* s = p.s + row * G;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int64_t c = (int64_t)(j * TPR + t) * VEC;
-      const bool in = c < p.cols;
-      float xh[VEC], o[VEC];
+      const int c = (j * TPR + t) * VEC;
+      float o[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        xh[i] = v[j * VEC + i] * rstd;
-        o[i] = xh[i] * w[j * VEC + i] + b[j * VEC + i];
+        float& xh = v[j * VEC + i];
+        xh *= rstd;
+        o[i] = p.w ? xh * w[j].get(i) : xh;
+        if (p.b) o[i] += b[j].get(i);
       }
-      if (in) store_vec<T, VEC>(y + c, o);
-      // a lane past the end still takes part in its group's maximum; its xh is NaN in a row whose
-      // rstd is, as is every other of that row
-      if (p.q) put_codes<VEC>(xh, in, c, p.q + row * p.cols, p.s + row * ((p.cols + 31) / 32));
+      store_chunk<T>(y + c, o, cols - c);
+      // a lane past the end still takes part in its group's maximum; its xh is NaN in a row whose rstd
+      // is, as is every other of that row
+      if (p.q) put_codes<VEC>(v + j * VEC, cols - c, c, q, s);
     }
   }
 }
@@ -255,106 +305,135 @@ template <class T>
 __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormParams p) {
   __shared__ float2 red[32];
   int phase = 0;
-  const int t = threadIdx.x;
-  const float n = (float)p.cols;  // divided by, so that a constant row's mean is exact
-  const int64_t ceil32 = (p.cols + 31) / 32 * 32;
+  const int t = threadIdx.x, cols = (int)p.cols, G = (cols + 31) >> 5;
+  const float n = (float)cols;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx;
     T* y = reinterpret_cast<T*>(p.y) + row * p.ldy;
     float sum = 0.0f;
-    for (int64_t c = t; c < p.cols; c += 1024) sum += Elem<T>::get(x[c]);
-    const float mean = row_sum<1024>(sum, red, phase) / n;
+    for (int c = t; c < cols; c += 1024) sum += Elem<T>::get(x[c]);
+    const float mean = row_sum<1024, 1024>(sum, red, phase) / n;
     float ss = 0.0f;
-    for (int64_t c = t; c < p.cols; c += 1024) {
+    for (int c = t; c < cols; c += 1024) {
       const float d = Elem<T>::get(x[c]) - mean;
       ss += d * d;
     }
-    const float rstd = 1.0f / sqrtf(row_sum<1024>(ss, red, phase) / n + p.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<1024, 1024>(ss, red, phase) / n + p.eps);
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
     }
-    for (int64_t c = t; c < ceil32; c += 1024) {  // whole groups: 32 lanes agree on the condition
-      const bool in = c < p.cols;
+    for (int c = t; c < 32 * G; c += 1024) {  // whole groups: 32 lanes agree on the condition
+      const bool in = c < cols;
       const float xh = in ? (Elem<T>::get(x[c]) - mean) * rstd : 0.0f;
       if (in) y[c] = Elem<T>::put(xh * weight_at(p.w, p.w_f32, c, 1.0f) + weight_at(p.b, p.w_f32, c, 0.0f));
-      if (p.q) put_codes<1>(&xh, in, c, p.q + row * p.cols, p.s + row * (ceil32 / 32));
+      if (p.q) put_codes<1>(&xh, cols - c, c, p.q + row * cols, p.s + row * G);
     }
   }
 }
 
 // ------------------------------------------------------------------ backward
 
-// One pass: dx, and this block's partial dw and db in row blockIdx.x of the workspace.
-template <class T, int VEC, int TPR, int NE, bool CK>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormParams p) {
-  constexpr int BLK = TPR > 256 ? TPR : 256;
-  constexpr int RPB = BLK / TPR;
-  constexpr int NC = NE / VEC;
-  __shared__ float2 red[TPR > 64 ? 2 * (TPR / 64) : 1];
+// One pass: dx, and (SUMS) this block's partial dw and db in row blockIdx.x of the workspace. Blocks of 1024
+// threads hold 1024 / TPR rows, so that one block per CU keeps enough loads in flight and leaves one partial
+// row: 256 partial rows cost 1/32 of the traffic of 8192 rows.
+template <class T, class W, int TPR, int NE, bool CK, bool SUMS>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
+  constexpr int BLK = 1024, RPB = BLK / TPR;
+  constexpr int VEC = Elem<T>::VEC, NC = NE / VEC;
+  __shared__ float2 red[2 * (BLK / 64)];
   int phase = 0;
-  const int t = threadIdx.x % TPR;
-  const float inv = 1.0f / (float)p.cols;
-  float w[NE], dw[NE], db[NE];
+  const int t = threadIdx.x % TPR, cols = (int)p.cols, G = (cols + 31) >> 5;
+  const float n = (float)cols;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row0 = (int64_t)blockIdx.x * RPB;  // the block's first row; all its threads walk together
+  const int sub = threadIdx.x / TPR;
+  // the next row: dy, x or its codes and scales, mean, rstd
+  Chunk<T, VEC> dyv[NC], xv[CK ? 1 : NC];
+  uint32_t kv[CK ? NC : 1][VEC / 4], sv[CK ? NC : 1];
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t r) {
+    const T* dy = reinterpret_cast<const T*>(p.dy) + r * p.ldy;
+    const T* x = CK ? nullptr : reinterpret_cast<const T*>(p.x) + r * p.ldx;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (j * TPR + t) * VEC;
+      dyv[j].load(dy + c, cols - c);
+      if constexpr (CK) {
+        const uint8_t* q = p.q + r * cols + c;
+        if (cols - c >= VEC) {
+          __builtin_memcpy(kv[j], q, VEC);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC / 4; ++i) kv[j][i] = 0;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (i < cols - c) kv[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
+        }
+        sv[j] = c < cols ? p.s[r * G + (c >> 5)] : 0u;
+      } else {
+        xv[j].load(x + c, cols - c);
+      }
+    }
+    if (!CK) mean = p.mean[r];
+    rstd = p.rstd[r];
+  };
+  Chunk<W, VEC> w[NC];
+  float dw[SUMS ? NE : 1], db[SUMS ? NE : 1];
+  if (row0 + sub < p.rows) fetch(row0 + sub);
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int64_t c = (int64_t)(j * TPR + t) * VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      w[j * VEC + i] = c < p.cols ? weight_at(p.w, p.w_f32, c + i, 1.0f) : 0.0f;
-      dw[j * VEC + i] = 0.0f;
-      db[j * VEC + i] = 0.0f;
-    }
+    const int c = (j * TPR + t) * VEC;
+    if (p.w) w[j].load(reinterpret_cast<const W*>(p.w) + c, cols - c);
   }
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < p.rows; row += (int64_t)gridDim.x * RPB) {
-    const T* dy = reinterpret_cast<const T*>(p.dy) + row * p.ldy;
-    const T* x = CK ? nullptr : reinterpret_cast<const T*>(p.x) + row * p.ldx;
-    const uint8_t* q = CK ? p.q + row * p.cols : nullptr;
-    const uint8_t* s = CK ? p.s + row * ((p.cols + 31) / 32) : nullptr;
-    T* dx = reinterpret_cast<T*>(p.dx) + row * p.lddx;
-    const float mean = CK ? 0.0f : p.mean[row];
-    const float rstd = p.rstd[row];
+#pragma unroll
+  for (int i = 0; i < (SUMS ? NE : 1); ++i) dw[i] = db[i] = 0.0f;
+  for (; row0 < p.rows; row0 += step) {
+    const int64_t row = row0 + sub;
+    const bool on = row < p.rows;  // (whole wavefronts)
     float g[NE], xh[NE];
     float c1 = 0.0f, c2 = 0.0f;
+    const float rs = rstd;
+    // (elements past the row's end have dy = 0 and add nothing)
+    if (on)
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int64_t c = (int64_t)(j * TPR + t) * VEC;
-      if (c < p.cols) {
-        load_vec<T, VEC>(dy + c, g + j * VEC);
-        if constexpr (CK)
-          get_codes<VEC>(q, s, c, xh + j * VEC);
-        else
-          load_vec<T, VEC>(x + c, xh + j * VEC);
+      Elem<T>::unpack(dyv[j].v[0], g + j * VEC);
+      const float sc = CK ? ckpt_scale(sv[j]) : 0.0f;
 #pragma unroll
-        for (int i = j * VEC; i < (j + 1) * VEC; ++i) {
-          if (!CK) xh[i] = (xh[i] - mean) * rstd;
-          dw[i] += g[i] * xh[i];
-          db[i] += g[i];
-          g[i] *= w[i];
-          c1 += g[i];
-          c2 += g[i] * xh[i];
+      for (int i = 0; i < VEC; ++i) {
+        const int k = j * VEC + i;
+        xh[k] = CK ? ckpt_value(kv[j], i, sc) : (xv[j].get(i) - mean) * rs;
+        if constexpr (SUMS) {
+          dw[k] += g[k] * xh[k];
+          db[k] += g[k];
         }
+        if (p.w) g[k] *= w[j].get(i);
+        c1 += g[k];
+        c2 += g[k] * xh[k];
       }
     }
-    row_sum2<TPR>(c1, c2, red, phase);
-    c1 *= inv;
-    c2 *= inv;
+    if (row + step < p.rows) fetch(row + step);
+    row_sum2<TPR, BLK>(c1, c2, red, phase);
+    if (!on) continue;
+    c1 /= n;
+    c2 /= n;
+    T* dx = reinterpret_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int64_t c = (int64_t)(j * TPR + t) * VEC;
-      if (c < p.cols) {
-        float o[VEC];
+      const int c = (j * TPR + t) * VEC;
+      float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = rstd * (g[j * VEC + i] - c1 - xh[j * VEC + i] * c2);
-        store_vec<T, VEC>(dx + c, o);
-      }
+      for (int i = 0; i < VEC; ++i) o[i] = rs * (g[j * VEC + i] - c1 - xh[j * VEC + i] * c2);
+      store_chunk<T>(dx + c, o, cols - c);
     }
   }
+  if constexpr (SUMS) {
   if (!p.part) return;
   // The wavefronts of a block that each walked their own rows add up in LDS, one after another.
-  float* pw = p.part + (int64_t)blockIdx.x * 2 * p.cols;
+  float* pw = p.part + (int64_t)blockIdx.x * 2 * cols;
   if constexpr (RPB > 1) {
-    __shared__ float acc[2][TPR * NE];
+    __shared__ float acc[2][SUMS ? TPR * NE : 1];
     for (int k = 0; k < RPB; ++k) {
       if (threadIdx.x / TPR == k) {
 #pragma unroll
@@ -374,25 +453,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormPar
   }
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int64_t c = (int64_t)(j * TPR + t) * VEC;
-    if (c < p.cols) {
+    const int c = (j * TPR + t) * VEC;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        pw[c + i] = dw[j * VEC + i];
-        pw[p.cols + c + i] = db[j * VEC + i];
-      }
+    for (int i = 0; i < VEC; i += 4) {
+      store_chunk<float>(pw + c + i, dw + j * VEC + i, cols - c - i);
+      store_chunk<float>(pw + cols + c + i, db + j * VEC + i, cols - c - i);
     }
+  }
   }
 }
 
-// Rows too long for registers: dx alone (two passes over a row), and the column sums by a second
-// kernel in which a thread owns a column.
+// Rows too long for registers: dx alone (two passes over a row). Past 8192 columns dw and db no longer fit
+// beside a row, and a second kernel forms the column sums, a thread per column.
 template <class T, bool CK>
 __device__ __forceinline__ float xhat_at(const NormParams& p, int64_t row, int64_t c, float mean, float rstd) {
   if constexpr (CK) {
-    float v;
-    get_codes<1>(p.q + row * p.cols, p.s + row * ((p.cols + 31) / 32), c, &v);
-    return v;
+    return __builtin_amdgcn_cvt_f32_fp8((int)p.q[row * p.cols + c], 0) *
+           ckpt_scale(p.s[row * ((p.cols + 31) / 32) + (c >> 5)]);
   } else {
     return (Elem<T>::get(reinterpret_cast<const T*>(p.x)[row * p.ldx + c]) - mean) * rstd;
   }
@@ -413,7 +490,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormParams p) {
       c1 += g;
       c2 += g * xhat_at<T, CK>(p, row, c, mean, rstd);
     }
-    row_sum2<1024>(c1, c2, red, phase);
+    row_sum2<1024, 1024>(c1, c2, red, phase);
     c1 *= inv;
     c2 *= inv;
     for (int64_t c = threadIdx.x; c < p.cols; c += 1024) {
@@ -439,20 +516,23 @@ __global__ __launch_bounds__(256) void norm_bwd_cols_kernel(NormParams p) {
   pw[p.cols + c] = db;
 }
 
-// dw and db as the sum of `parts` partial rows, 64 columns a block and 16 rows at a time; the order of
+// dw and db as the sum of `parts` partial rows, 32 columns a block and 32 rows at a time; the order of
 // the additions depends on `parts` alone.
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, int parts, int64_t cols, float* dw,
                                                            float* db) {
-  __shared__ float acc[16][64];
-  const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);  // over dw's columns, then db's
-  const int r = threadIdx.x >> 6;
+  __shared__ float acc[32][33];
+  const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);  // over dw's columns, then db's
+  const int r = threadIdx.x >> 5;
   float v = 0.0f;
-  if (c < 2 * cols)
-    for (int i = r; i < parts; i += 16) v += part[(int64_t)i * 2 * cols + c];
-  acc[r][threadIdx.x & 63] = v;
+  if (c < 2 * cols) {
+#pragma unroll 8
+    for (int i = r; i < parts; i += 32) v += part[(int64_t)i * 2 * cols + c];
+  }
+  acc[r][threadIdx.x & 31] = v;
   __syncthreads();
   if (r == 0 && c < 2 * cols) {
-    for (int i = 1; i < 16; ++i) v += acc[i][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) v += acc[i][threadIdx.x];
     float* out = c < cols ? dw : db;
     if (out) out[c < cols ? c : c - cols] = v;
   }
@@ -466,96 +546,70 @@ namespace {
 
 using mxf::NormParams;
 
-bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Threads per row and elements per thread for a width; {0, 0}: longer than registers hold.
 struct NormShape {
   int tpr, ne;
+  int key() const { return tpr * 100 + ne; }
 };
+// Eight elements per thread up to 8192 columns: the next row's loads in flight and enough wavefronts per CU;
+// with 32 per thread (a wavefront per row of 2048, no barrier) the registers left two wavefronts per
+// SIMD and the forward measured TODO.
 NormShape norm_shape(int64_t cols) {
   if (cols <= 512) return {64, 8};
-  if (cols <= 1024) return {64, 16};
-  if (cols <= 2048) return {64, 32};
-  if (cols <= 4096) return {256, 16};
-  if (cols <= 8192) return {256, 32};
+  if (cols <= 1024) return {128, 8};
+  if (cols <= 2048) return {256, 8};
+  if (cols <= 4096) return {512, 8};
+  if (cols <= 8192) return {1024, 8};
   if (cols <= 16384) return {1024, 16};
   return {0, 0};
 }
 
-bool norm_vec(const NormParams& p, int esz) {
-  const int64_t v = 16 / esz;
-  bool ok = p.cols % v == 0;
-  if (p.x) ok = ok && a16(p.x) && p.ldx % v == 0;
-  if (p.y) ok = ok && a16(p.y) && p.ldy % v == 0;
-  if (p.dy) ok = ok && a16(p.dy) && p.ldy % v == 0;
-  if (p.dx) ok = ok && a16(p.dx) && p.lddx % v == 0;
-  if (p.q) ok = ok && a16(p.q);
-  return ok;
+template <class T, class W>
+void launch_fwd(const NormParams& p, hipStream_t st) {
+  NormShape s = norm_shape(p.cols);
+  if (s.tpr == 128) s.tpr = 256;  // one row per block, half of its lanes idle at most
+  const int blk = s.tpr > 256 ? s.tpr : s.tpr ? 256 : 1024;
+  const int64_t rpb = s.tpr == 64 ? 4 : 1, need = (p.rows + rpb - 1) / rpb, most = 256 * 2048 / blk;
+  const dim3 g((unsigned)(need < most ? need : most)), b(blk);
+  switch (s.key()) {
+    case 6408: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 64, 8>), g, b, 0, st, p); break;
+    case 25608: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 256, 8>), g, b, 0, st, p); break;
+    case 51208: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 512, 8>), g, b, 0, st, p); break;
+    case 102408: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 1024, 8>), g, b, 0, st, p); break;
+    case 102416: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 1024, 16>), g, b, 0, st, p); break;
+    default: hipLaunchKernelGGL((mxf::norm_fwd_long_kernel<T>), g, b, 0, st, p);
+  }
 }
 
-template <int TPR, int NE>
-void launch_fwd(const NormParams& p, bool f32, bool vec, int64_t blocks, hipStream_t st) {
-  const dim3 g((unsigned)blocks), b(TPR > 256 ? TPR : 256);
-  if (f32)
-    hipLaunchKernelGGL((vec ? mxf::norm_fwd_kernel<float, 4, TPR, NE>
-             : mxf::norm_fwd_kernel<float, 1, TPR, NE>),
-        g, b, 0, st, p);
-  else
-    hipLaunchKernelGGL((vec ? mxf::norm_fwd_kernel<uint16_t, 8, TPR, NE>
-             : mxf::norm_fwd_kernel<uint16_t, 1, TPR, NE>),
-        g, b, 0, st, p);
-}
-
-template <int TPR, int NE, bool CK>
-void launch_bwd(const NormParams& p, bool f32, bool vec, int64_t blocks, hipStream_t st) {
-  const dim3 g((unsigned)blocks), b(TPR > 256 ? TPR : 256);
-  if (f32)
-    hipLaunchKernelGGL((vec ? mxf::norm_bwd_kernel<float, 4, TPR, NE, CK>
-             : mxf::norm_bwd_kernel<float, 1, TPR, NE, CK>),
-        g, b, 0, st, p);
-  else
-    hipLaunchKernelGGL((vec ? mxf::norm_bwd_kernel<uint16_t, 8, TPR, NE, CK>
-             : mxf::norm_bwd_kernel<uint16_t, 1, TPR, NE, CK>),
-        g, b, 0, st, p);
-}
-
-template <bool CK>
-hipError_t norm_bwd_any(const NormParams& p, bool f32, bool vec, int64_t blocks, int parts, hipStream_t st) {
+template <class T, class W, bool CK>
+hipError_t launch_bwd(const NormParams& p, int parts, hipStream_t st) {
   const NormShape s = norm_shape(p.cols);
-  switch (s.tpr * 100 + s.ne) {
-    case 6408: launch_bwd<64, 8, CK>(p, f32, vec, blocks, st); break;
-    case 6416: launch_bwd<64, 16, CK>(p, f32, vec, blocks, st); break;
-    case 6432: launch_bwd<64, 32, CK>(p, f32, vec, blocks, st); break;
-    case 25616: launch_bwd<256, 16, CK>(p, f32, vec, blocks, st); break;
-    case 25632: launch_bwd<256, 32, CK>(p, f32, vec, blocks, st); break;
-    case 102416:
-      if (vec) {
-        const dim3 g((unsigned)blocks);
-        if (f32)
-          hipLaunchKernelGGL((mxf::norm_bwd_kernel<float, 4, 1024, 16, CK>), g, dim3(1024), 0, st, p);
-        else
-          hipLaunchKernelGGL((mxf::norm_bwd_kernel<uint16_t, 8, 1024, 16, CK>), g, dim3(1024), 0, st, p);
-        break;
-      }
-      [[fallthrough]];  // one element per load needs more registers than 1024 threads have
+  const dim3 g((unsigned)parts), b(1024);
+  switch (s.key()) {
+    case 6408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 64, 8, CK, true>), g, b, 0, st, p); break;
+    case 12808: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 128, 8, CK, true>), g, b, 0, st, p); break;
+    case 25608: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 256, 8, CK, true>), g, b, 0, st, p); break;
+    case 51208: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 512, 8, CK, true>), g, b, 0, st, p); break;
+    case 102408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 1024, 8, CK, true>), g, b, 0, st, p); break;
     default: {
-      const dim3 cg((unsigned)((p.cols + 255) / 256), (unsigned)parts);
       if (p.part) {
-        if (f32)
-          hipLaunchKernelGGL((mxf::norm_bwd_cols_kernel<float, CK>), cg, dim3(256), 0, st, p);
-        else
-          hipLaunchKernelGGL((mxf::norm_bwd_cols_kernel<uint16_t, CK>), cg, dim3(256), 0, st, p);
+        hipLaunchKernelGGL((mxf::norm_bwd_cols_kernel<T, CK>), dim3((unsigned)((p.cols + 255) / 256), (unsigned)parts),
+                           dim3(256), 0, st, p);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
       }
-      const dim3 rg((unsigned)(p.rows < 4096 ? p.rows : 4096));
-      if (f32)
-        hipLaunchKernelGGL((mxf::norm_bwd_long_kernel<float, CK>), rg, dim3(1024), 0, st, p);
+      const dim3 rg((unsigned)(p.rows < 512 ? p.rows : 512));
+      if (s.tpr)
+        hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 1024, 16, CK, false>), rg, b, 0, st, p);
       else
-        hipLaunchKernelGGL((mxf::norm_bwd_long_kernel<uint16_t, CK>), rg, dim3(1024), 0, st, p);
+        hipLaunchKernelGGL((mxf::norm_bwd_long_kernel<T, CK>), rg, b, 0, st, p);
     }
   }
   return hipGetLastError();
+}
+template <class T, class W>
+hipError_t launch_bwd_any(const NormParams& p, int parts, hipStream_t st) {
+  return p.q ? launch_bwd<T, W, true>(p, parts, st) : launch_bwd<T, W, false>(p, parts, st);
 }
 
 }  // namespace
@@ -563,43 +617,31 @@ hipError_t norm_bwd_any(const NormParams& p, bool f32, bool vec, int64_t blocks,
 // Blocks of the backward, which is also the number of partial rows.
 int mxf_norm_parts(int64_t rows, int64_t cols) {
   const NormShape s = norm_shape(cols);
-  if (!s.tpr) return (int)(rows < 32 ? rows : 32);
-  const int64_t need = s.tpr == 64 ? (rows + 3) / 4 : rows;
-  return (int)(need < 512 ? need : 512);
+  const bool one = s.ne == 8;  // dx and the column sums in one kernel
+  const int64_t need = one ? (rows + 1024 / s.tpr - 1) / (1024 / s.tpr) : rows;
+  const int64_t most = one ? 256 : 128;
+  return (int)(need < most ? need : most);
 }
 
 hipError_t mxf_launch_norm_fwd(const NormParams& p, bool f32, hipStream_t st) {
-  const NormShape s = norm_shape(p.cols);
-  const bool vec = norm_vec(p, f32 ? 4 : 2);
-  const int64_t need = s.tpr == 64 ? (p.rows + 3) / 4 : p.rows;
-  const int64_t blocks = need < 2048 ? need : 2048;
-  switch (s.tpr * 100 + s.ne) {
-    case 6408: launch_fwd<64, 8>(p, f32, vec, blocks, st); break;
-    case 6416: launch_fwd<64, 16>(p, f32, vec, blocks, st); break;
-    case 6432: launch_fwd<64, 32>(p, f32, vec, blocks, st); break;
-    case 25616: launch_fwd<256, 16>(p, f32, vec, blocks, st); break;
-    case 25632: launch_fwd<256, 32>(p, f32, vec, blocks, st); break;
-    case 102416: launch_fwd<1024, 16>(p, f32, vec, blocks, st); break;
-    default:
-      if (f32)
-        hipLaunchKernelGGL(mxf::norm_fwd_long_kernel<float>, dim3((unsigned)blocks), dim3(1024), 0, st, p);
-      else
-        hipLaunchKernelGGL(mxf::norm_fwd_long_kernel<uint16_t>, dim3((unsigned)blocks), dim3(1024), 0, st, p);
-  }
+  if (f32)
+    p.w_f32 ? launch_fwd<float, float>(p, st) : launch_fwd<float, uint16_t>(p, st);
+  else
+    p.w_f32 ? launch_fwd<uint16_t, float>(p, st) : launch_fwd<uint16_t, uint16_t>(p, st);
   return hipGetLastError();
 }
 
 // p.part: the workspace, or null where neither dw nor db is wanted.
 hipError_t mxf_launch_norm_bwd(const NormParams& p, bool f32, hipStream_t st) {
-  const bool vec = norm_vec(p, f32 ? 4 : 2);
   const int parts = mxf_norm_parts(p.rows, p.cols);
   if (p.rows > 0) {
-    hipError_t e = p.q ? norm_bwd_any<true>(p, f32, vec, parts, parts, st)
-                       : norm_bwd_any<false>(p, f32, vec, parts, parts, st);
+    hipError_t e = f32 ? (p.w_f32 ? launch_bwd_any<float, float>(p, parts, st) : launch_bwd_any<float, uint16_t>(p, parts, st))
+                       : (p.w_f32 ? launch_bwd_any<uint16_t, float>(p, parts, st)
+                                  : launch_bwd_any<uint16_t, uint16_t>(p, parts, st));
     if (e != hipSuccess) return e;
   }
   if (!p.part) return hipSuccess;
-  hipLaunchKernelGGL(mxf::norm_reduce_kernel, dim3((unsigned)((2 * p.cols + 63) / 64)), dim3(1024), 0, st, p.part,
+  hipLaunchKernelGGL(mxf::norm_reduce_kernel, dim3((unsigned)((2 * p.cols + 31) / 32)), dim3(1024), 0, st, p.part,
                      parts, p.cols, p.dw, p.db);
   return hipGetLastError();
 }
