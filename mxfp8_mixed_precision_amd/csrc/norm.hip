@@ -28,6 +28,9 @@
 
 namespace mxf {
 
+__device__ __forceinline__ uint32_t bits_of(uint16_t v) { return v; }
+__device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
+
 template <class T>
 struct Elem;
 template <>
@@ -60,48 +63,31 @@ struct Elem<float> {
   }
 };
 
-// N elements at p as FP32, of which the first n exist (n >= N: all); the others are zero.
-template <class T, int N>
-struct Chunk {
-  static constexpr int B = N * (int)sizeof(T), W = (B + 15) / 16;
-  u32x4_t v[W];
-  __device__ __forceinline__ void load(const T* p, int n) {
-    if (n >= N) {
-      if constexpr (B >= 16) {
-        __builtin_memcpy(v, p, B);
-      } else {
-        v[0] = (u32x4_t){0, 0, 0, 0};
-        __builtin_memcpy(v, p, B);
-      }
-      return;
-    }
+// 16 bytes of a row as loaded, of which the first n elements exist (n >= VEC: all); the others are zero. EXACT:
+// rows end on a chunk, so n is all or none.
+template <class T, bool EXACT>
+__device__ __forceinline__ u32x4_t load_chunk(const T* p, int n) {
+  u32x4_t v = {0, 0, 0, 0};
+  if (EXACT ? n > 0 : n >= Elem<T>::VEC) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (!EXACT && n > 0) {
+    uint32_t e[Elem<T>::VEC];
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = (u32x4_t){0, 0, 0, 0};
-    if (n <= 0) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) {
-        if constexpr (sizeof(T) == 4)
-          v[i / 4][i % 4] = __builtin_bit_cast(uint32_t, p[i]);
-        else
-          v[i / 8][i % 8 / 2] |= (uint32_t)p[i] << (16 * (i % 2));
-      }
-  }
-  __device__ __forceinline__ float get(int i) const {
+    for (int i = 0; i < Elem<T>::VEC; ++i) e[i] = i < n ? bits_of(p[i]) : 0u;
     if constexpr (sizeof(T) == 4)
-      return __uint_as_float(v[i / 4][i % 4]);
+      v = (u32x4_t){e[0], e[1], e[2], e[3]};
     else
-      return i % 2 ? bf16_hi(v[i / 8][i % 8 / 2]) : bf16_lo(v[i / 8][i % 8 / 2]);
+      v = (u32x4_t){e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
   }
-};
-
-template <class T>
+  return v;
+}
+template <class T, bool EXACT>
 __device__ __forceinline__ void store_chunk(T* p, const float* f, int n) {
   constexpr int VEC = Elem<T>::VEC;
-  if (n >= VEC) {
+  if (EXACT ? n > 0 : n >= VEC) {
     const u32x4_t v = Elem<T>::pack(f);
     __builtin_memcpy(p, &v, 16);
-  } else {
+  } else if (!EXACT) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       if (i < n) p[i] = Elem<T>::put(f[i]);
@@ -114,10 +100,52 @@ __device__ __forceinline__ float weight_at(const void* w, bool f32, int64_t c, f
   return f32 ? reinterpret_cast<const float*>(w)[c] : Elem<uint16_t>::get(reinterpret_cast<const uint16_t*>(w)[c]);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// NE weights of this thread's columns as FP32 (FP32, BF16 or absent: then `none`), once per block.
+template <int VEC, int TPR, int NE>
+__device__ __forceinline__ void load_weights(const void* w, bool f32, int t, int cols, float none, float* f) {
 #pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  for (int j = 0; j < NE / VEC; ++j) {
+    const int c = (j * TPR + t) * VEC;
+    if (w && c + VEC <= cols) {
+      if (f32) {
+        __builtin_memcpy(f + j * VEC, reinterpret_cast<const float*>(w) + c, VEC * 4);
+      } else {
+        uint32_t k[VEC / 2];
+        __builtin_memcpy(k, reinterpret_cast<const uint16_t*>(w) + c, VEC * 2);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[j * VEC + i] = i % 2 ? bf16_hi(k[i / 2]) : bf16_lo(k[i / 2]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f[j * VEC + i] = c + i < cols ? weight_at(w, f32, c + i, none) : 0.0f;
+    }
+  }
+}
+
+// Lane exchanges on the vector ALU (DPP), a few cycles each; through the LDS crossbar a row's six steps
+// took longer than everything else between its loads and its stores. CTRL: 0xB1 lane ^ 1, 0x4E lane ^ 2,
+// 0x141 mirror in 8 (once 4 lanes agree: the other 4), 0x140 mirror in 16, 0x142 / 0x143 the last lane
+// of row 0, 2 / of lane 31 to the rows above.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ uint32_t dpp_half_mirror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);
+}
+template <int N>  // sum over N lanes (a power of two, at most 16), in all of them
+__device__ __forceinline__ float lanes_sum(float v) {
+  if (N >= 2) v = dpp_add<0xB1>(v);
+  if (N >= 4) v = dpp_add<0x4E>(v);
+  if (N >= 8) v = dpp_add<0x141>(v);
+  if (N >= 16) v = dpp_add<0x140>(v);
   return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = lanes_sum<16>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  v = dpp_add<0x143, 0xC>(v);
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 // Sum of a pair over the TPR threads of a row; a block of BLK threads holds BLK / TPR rows. TPR 64 is one
@@ -128,33 +156,26 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float2* red, int& p
   a = wave_sum(a);
   b = wave_sum(b);
   if constexpr (TPR > 64) {
+    constexpr int NW = TPR / 64;
     float2* slot = red + phase * (BLK / 64);
     phase ^= 1;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = make_float2(a, b);
     __syncthreads();
-    slot += threadIdx.x / TPR * (TPR / 64);
-    a = 0.0f;
-    b = 0.0f;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) {
-      const float2 v = slot[i];
-      a += v.x;
-      b += v.y;
-    }
+    const float2 v = slot[threadIdx.x / TPR * NW + (threadIdx.x & (NW - 1))];
+    a = lanes_sum<NW>(v.x);
+    b = lanes_sum<NW>(v.y);
   }
 }
 template <int TPR, int BLK>
 __device__ __forceinline__ float row_sum(float a, float2* red, int& phase) {
   a = wave_sum(a);
   if constexpr (TPR > 64) {
+    constexpr int NW = TPR / 64;
     float2* slot = red + phase * (BLK / 64);
     phase ^= 1;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6].x = a;
     __syncthreads();
-    slot += threadIdx.x / TPR * (TPR / 64);
-    a = 0.0f;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) a += slot[i].x;
+    a = lanes_sum<NW>(slot[threadIdx.x / TPR * NW + (threadIdx.x & (NW - 1))].x);
   }
   return a;
 }
@@ -165,7 +186,7 @@ template <int VEC>
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
   m = max(m, dpp_xor1(m));
   m = max(m, dpp_xor2(m));
-  if constexpr (VEC < 8) m = max(m, (uint32_t)__shfl_xor((int)m, 4));
+  if constexpr (VEC < 8) m = max(m, dpp_half_mirror(m));
   if constexpr (VEC < 4) {
     m = max(m, (uint32_t)__shfl_xor((int)m, 8));
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));
@@ -175,7 +196,7 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
 
 // Quantize VEC normalised values, of which the first n exist (the others are zero), and store codes and the
 // group's scale at column c. Every lane of the group calls this.
-template <int VEC>
+template <int VEC, bool EXACT>
 __device__ __forceinline__ void put_codes(const float* xh, int n, int c, uint8_t* q, uint8_t* s) {
   if constexpr (VEC == 1) {
     const uint32_t v = bf16_bits(xh[0]);
@@ -194,9 +215,9 @@ __device__ __forceinline__ void put_codes(const float* xh, int n, int c, uint8_t
     const Scale sc = scale_from_amax(group_max<VEC>(max(m & 0xFFFFu, m >> 16)));
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) k[i] = cvt4(w[2 * i], w[2 * i + 1], sc);
-    if (n >= VEC) {
+    if (EXACT ? n > 0 : n >= VEC) {
       __builtin_memcpy(q + c, k, VEC);
-    } else {
+    } else if (!EXACT) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         if (i < n) q[c + i] = (uint8_t)(k[i / 4] >> (8 * (i % 4)));
@@ -220,41 +241,36 @@ __device__ __forceinline__ float ckpt_value(const uint32_t* k, int i, float sc) 
 
 // ------------------------------------------------------------------ forward
 
-template <class T, class W, int TPR, int NE>
+template <class T, int TPR, int NE, bool EXACT>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormParams p) {
   constexpr int BLK = TPR > 256 ? TPR : 256, RPB = BLK / TPR;  // rows in flight per block
   static_assert(TPR == 64 || RPB == 1, "rows of several wavefronts have a block of their own");
   constexpr int VEC = Elem<T>::VEC, NC = NE / VEC;             // chunks per thread
   __shared__ float2 red[2 * (BLK / 64)];
   int phase = 0;
-  const int t = threadIdx.x % TPR, cols = (int)p.cols;
+  const int t = threadIdx.x % TPR, cols = (int)p.cols, G = (cols + 31) >> 5;
   const float n = (float)cols;  // divided by, so that a constant row's mean is exact
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  Chunk<T, VEC> x[NC];
-  Chunk<W, VEC> w[NC], b[NC];
+  u32x4_t x[NC];  // the next row
   auto fetch = [&](int64_t r) {
     const T* src = reinterpret_cast<const T*>(p.x) + r * p.ldx;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * TPR + t) * VEC;
-      x[j].load(src + c, cols - c);
+      x[j] = load_chunk<T, EXACT>(src + c, cols - c);
     }
   };
+  float w[NE], b[NE];
   if (row < p.rows) fetch(row);
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = (j * TPR + t) * VEC;
-    if (p.w) w[j].load(reinterpret_cast<const W*>(p.w) + c, cols - c);
-    if (p.b) b[j].load(reinterpret_cast<const W*>(p.b) + c, cols - c);
-  }
-  const int G = (cols + 31) >> 5;
+  load_weights<VEC, TPR, NE>(p.w, p.w_f32, t, cols, 1.0f, w);
+  load_weights<VEC, TPR, NE>(p.b, p.w_f32, t, cols, 0.0f, b);
   for (; row < p.rows; row += step) {
     float v[NE];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      Elem<T>::unpack(x[j].v[0], v + j * VEC);
+      Elem<T>::unpack(x[j], v + j * VEC);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) sum += v[j * VEC + i];
     }
@@ -264,22 +280,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormPar
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int m = cols - (j * TPR + t) * VEC;
-      const bool whole = (j + 1) * TPR * VEC <= cols;  // for every lane
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         float& d = v[j * VEC + i];
-        d = whole || i < m ? d - mean : 0.0f;
+        d = (EXACT ? m > 0 : i < m) ? d - mean : 0.0f;
         ss += d * d;
       }
     }
     const float rstd = 1.0f / sqrtf(row_sum<TPR, BLK>(ss, red, phase) / n + p.eps);
+    // The next row's loads end here, before this row's stores are issued: loads and stores are counted in
+    // order, so a wait for the loads after them would wait for the stores as well.
+#pragma unroll
+    for (int j = 0; j < NC; ++j) asm volatile("" : "+v"(x[j]));
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
     }
     T* y = reinterpret_cast<T*>(p.y) + row * p.ldy;
-    uint8_t* q = p.q + row * cols;
-    uint8_t* s = p.s + row * G;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * TPR + t) * VEC;
@@ -288,13 +305,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormPar
       for (int i = 0; i < VEC; ++i) {
         float& xh = v[j * VEC + i];
         xh *= rstd;
-        o[i] = p.w ? xh * w[j].get(i) : xh;
-        if (p.b) o[i] += b[j].get(i);
+        o[i] = xh * w[j * VEC + i] + b[j * VEC + i];
       }
-      store_chunk<T>(y + c, o, cols - c);
+      store_chunk<T, EXACT>(y + c, o, cols - c);
       // a lane past the end still takes part in its group's maximum; its xh is NaN in a row whose rstd
       // is, as is every other of that row
-      if (p.q) put_codes<VEC>(v + j * VEC, cols - c, c, q, s);
+      if (p.q) put_codes<VEC, EXACT>(v + j * VEC, cols - c, c, p.q + row * cols, p.s + row * G);
     }
   }
 }
@@ -327,7 +343,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormParams p) {
       const bool in = c < cols;
       const float xh = in ? (Elem<T>::get(x[c]) - mean) * rstd : 0.0f;
       if (in) y[c] = Elem<T>::put(xh * weight_at(p.w, p.w_f32, c, 1.0f) + weight_at(p.b, p.w_f32, c, 0.0f));
-      if (p.q) put_codes<1>(&xh, cols - c, c, p.q + row * cols, p.s + row * G);
+      if (p.q) put_codes<1, false>(&xh, cols - c, c, p.q + row * cols, p.s + row * G);
     }
   }
 }
@@ -337,7 +353,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormParams p) {
 // One pass: dx, and (SUMS) this block's partial dw and db in row blockIdx.x of the workspace. Blocks of 1024
 // threads hold 1024 / TPR rows, so that one block per CU keeps enough loads in flight and leaves one partial
 // row: 256 partial rows cost 1/32 of the traffic of 8192 rows.
-template <class T, class W, int TPR, int NE, bool CK, bool SUMS>
+template <class T, int TPR, int NE, bool CK, bool SUMS, bool EXACT>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
   constexpr int BLK = 1024, RPB = BLK / TPR;
   constexpr int VEC = Elem<T>::VEC, NC = NE / VEC;
@@ -349,7 +365,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
   int64_t row0 = (int64_t)blockIdx.x * RPB;  // the block's first row; all its threads walk together
   const int sub = threadIdx.x / TPR;
   // the next row: dy, x or its codes and scales, mean, rstd
-  Chunk<T, VEC> dyv[NC], xv[CK ? 1 : NC];
+  u32x4_t dyv[NC], xv[CK ? 1 : NC];
   uint32_t kv[CK ? NC : 1][VEC / 4], sv[CK ? NC : 1];
   float mean = 0.0f, rstd = 0.0f;
   auto fetch = [&](int64_t r) {
@@ -357,35 +373,30 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
     const T* x = CK ? nullptr : reinterpret_cast<const T*>(p.x) + r * p.ldx;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int c = (j * TPR + t) * VEC;
-      dyv[j].load(dy + c, cols - c);
+      const int c = (j * TPR + t) * VEC, m = cols - c;
+      dyv[j] = load_chunk<T, EXACT>(dy + c, m);
       if constexpr (CK) {
         const uint8_t* q = p.q + r * cols + c;
-        if (cols - c >= VEC) {
-          __builtin_memcpy(kv[j], q, VEC);
-        } else {
 #pragma unroll
-          for (int i = 0; i < VEC / 4; ++i) kv[j][i] = 0;
+        for (int i = 0; i < VEC / 4; ++i) kv[j][i] = 0;
+        if (EXACT ? m > 0 : m >= VEC) {
+          __builtin_memcpy(kv[j], q, VEC);
+        } else if (!EXACT) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i)
-            if (i < cols - c) kv[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
+            if (i < m) kv[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
         }
-        sv[j] = c < cols ? p.s[r * G + (c >> 5)] : 0u;
+        sv[j] = m > 0 ? p.s[r * G + (c >> 5)] : 0u;
       } else {
-        xv[j].load(x + c, cols - c);
+        xv[j] = load_chunk<T, EXACT>(x + c, m);
       }
     }
     if (!CK) mean = p.mean[r];
     rstd = p.rstd[r];
   };
-  Chunk<W, VEC> w[NC];
-  float dw[SUMS ? NE : 1], db[SUMS ? NE : 1];
+  float w[NE], dw[SUMS ? NE : 1], db[SUMS ? NE : 1];
   if (row0 + sub < p.rows) fetch(row0 + sub);
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = (j * TPR + t) * VEC;
-    if (p.w) w[j].load(reinterpret_cast<const W*>(p.w) + c, cols - c);
-  }
+  load_weights<VEC, TPR, NE>(p.w, p.w_f32, t, cols, 1.0f, w);
 #pragma unroll
   for (int i = 0; i < (SUMS ? NE : 1); ++i) dw[i] = db[i] = 0.0f;
   for (; row0 < p.rows; row0 += step) {
@@ -394,30 +405,43 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
     float g[NE], xh[NE];
     float c1 = 0.0f, c2 = 0.0f;
     const float rs = rstd;
-    // (elements past the row's end have dy = 0 and add nothing)
-    if (on)
+    if (on) {  // (elements past the row's end have dy = 0 and add nothing)
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      Elem<T>::unpack(dyv[j].v[0], g + j * VEC);
-      const float sc = CK ? ckpt_scale(sv[j]) : 0.0f;
+      for (int j = 0; j < NC; ++j) {
+        float xf[VEC];
+        Elem<T>::unpack(dyv[j], g + j * VEC);
+        if (!CK) Elem<T>::unpack(xv[CK ? 0 : j], xf);
+        const float sc = CK ? ckpt_scale(sv[j]) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int k = j * VEC + i;
-        xh[k] = CK ? ckpt_value(kv[j], i, sc) : (xv[j].get(i) - mean) * rs;
-        if constexpr (SUMS) {
-          dw[k] += g[k] * xh[k];
-          db[k] += g[k];
+        for (int i = 0; i < VEC; ++i) {
+          const int k = j * VEC + i;
+          xh[k] = CK ? ckpt_value(kv[j], i, sc) : (xf[i] - mean) * rs;
+          if constexpr (SUMS) {
+            dw[k] += g[k] * xh[k];
+            db[k] += g[k];
+          }
+          g[k] *= w[k];
+          c1 += g[k];
+          c2 += g[k] * xh[k];
         }
-        if (p.w) g[k] *= w[j].get(i);
-        c1 += g[k];
-        c2 += g[k] * xh[k];
       }
     }
     if (row + step < p.rows) fetch(row + step);
     row_sum2<TPR, BLK>(c1, c2, red, phase);
-    if (!on) continue;
     c1 /= n;
     c2 /= n;
+    // (the next row's loads end before this row's stores are issued, as in the forward)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      asm volatile("" : "+v"(dyv[j]));
+      if constexpr (CK) {
+        asm volatile("" : "+v"(kv[j][0]), "+v"(sv[j]));
+        if constexpr (VEC == 8) asm volatile("" : "+v"(kv[j][1]));
+      } else {
+        asm volatile("" : "+v"(xv[j]));
+      }
+    }
+    if (!on) continue;
     T* dx = reinterpret_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -425,41 +449,41 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
       float o[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) o[i] = rs * (g[j * VEC + i] - c1 - xh[j * VEC + i] * c2);
-      store_chunk<T>(dx + c, o, cols - c);
+      store_chunk<T, EXACT>(dx + c, o, cols - c);
     }
   }
   if constexpr (SUMS) {
-  if (!p.part) return;
-  // The wavefronts of a block that each walked their own rows add up in LDS, one after another.
-  float* pw = p.part + (int64_t)blockIdx.x * 2 * cols;
-  if constexpr (RPB > 1) {
-    __shared__ float acc[2][SUMS ? TPR * NE : 1];
-    for (int k = 0; k < RPB; ++k) {
-      if (threadIdx.x / TPR == k) {
+    if (!p.part) return;
+    // The rows of a block add up in LDS, one after another.
+    float* pw = p.part + (int64_t)blockIdx.x * 2 * cols;
+    if constexpr (RPB > 1) {
+      __shared__ float acc[2][TPR * NE];
+      for (int k = 0; k < RPB; ++k) {
+        if (sub == k) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          acc[0][i * TPR + t] = k ? acc[0][i * TPR + t] + dw[i] : dw[i];
-          acc[1][i * TPR + t] = k ? acc[1][i * TPR + t] + db[i] : db[i];
+          for (int i = 0; i < NE; ++i) {
+            acc[0][i * TPR + t] = k ? acc[0][i * TPR + t] + dw[i] : dw[i];
+            acc[1][i * TPR + t] = k ? acc[1][i * TPR + t] + db[i] : db[i];
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
-    }
-    if (threadIdx.x >= TPR) return;
+      if (threadIdx.x >= TPR) return;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      dw[i] = acc[0][i * TPR + t];
-      db[i] = acc[1][i * TPR + t];
+      for (int i = 0; i < NE; ++i) {
+        dw[i] = acc[0][i * TPR + t];
+        db[i] = acc[1][i * TPR + t];
+      }
     }
-  }
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = (j * TPR + t) * VEC;
+    for (int j = 0; j < NC; ++j) {
+      const int c = (j * TPR + t) * VEC;
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      store_chunk<float>(pw + c + i, dw + j * VEC + i, cols - c - i);
-      store_chunk<float>(pw + cols + c + i, db + j * VEC + i, cols - c - i);
+      for (int i = 0; i < VEC; i += 4) {
+        store_chunk<float, false>(pw + c + i, dw + j * VEC + i, cols - c - i);
+        store_chunk<float, false>(pw + cols + c + i, db + j * VEC + i, cols - c - i);
+      }
     }
-  }
   }
 }
 
@@ -564,7 +588,7 @@ NormShape norm_shape(int64_t cols) {
   return {0, 0};
 }
 
-template <class T, class W>
+template <class T, bool EXACT>
 void launch_fwd(const NormParams& p, hipStream_t st) {
   NormShape s = norm_shape(p.cols);
   if (s.tpr == 128) s.tpr = 256;  // one row per block, half of its lanes idle at most
@@ -572,25 +596,25 @@ void launch_fwd(const NormParams& p, hipStream_t st) {
   const int64_t rpb = s.tpr == 64 ? 4 : 1, need = (p.rows + rpb - 1) / rpb, most = 256 * 2048 / blk;
   const dim3 g((unsigned)(need < most ? need : most)), b(blk);
   switch (s.key()) {
-    case 6408: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 64, 8>), g, b, 0, st, p); break;
-    case 25608: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 256, 8>), g, b, 0, st, p); break;
-    case 51208: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 512, 8>), g, b, 0, st, p); break;
-    case 102408: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 1024, 8>), g, b, 0, st, p); break;
-    case 102416: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, W, 1024, 16>), g, b, 0, st, p); break;
+    case 6408: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 64, 8, EXACT>), g, b, 0, st, p); break;
+    case 25608: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 256, 8, EXACT>), g, b, 0, st, p); break;
+    case 51208: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 512, 8, EXACT>), g, b, 0, st, p); break;
+    case 102408: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 1024, 8, EXACT>), g, b, 0, st, p); break;
+    case 102416: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 1024, 16, EXACT>), g, b, 0, st, p); break;
     default: hipLaunchKernelGGL((mxf::norm_fwd_long_kernel<T>), g, b, 0, st, p);
   }
 }
 
-template <class T, class W, bool CK>
+template <class T, bool CK, bool EXACT>
 hipError_t launch_bwd(const NormParams& p, int parts, hipStream_t st) {
   const NormShape s = norm_shape(p.cols);
   const dim3 g((unsigned)parts), b(1024);
   switch (s.key()) {
-    case 6408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 64, 8, CK, true>), g, b, 0, st, p); break;
-    case 12808: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 128, 8, CK, true>), g, b, 0, st, p); break;
-    case 25608: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 256, 8, CK, true>), g, b, 0, st, p); break;
-    case 51208: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 512, 8, CK, true>), g, b, 0, st, p); break;
-    case 102408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 1024, 8, CK, true>), g, b, 0, st, p); break;
+    case 6408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 64, 8, CK, true, EXACT>), g, b, 0, st, p); break;
+    case 12808: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 128, 8, CK, true, EXACT>), g, b, 0, st, p); break;
+    case 25608: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 256, 8, CK, true, EXACT>), g, b, 0, st, p); break;
+    case 51208: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 512, 8, CK, true, EXACT>), g, b, 0, st, p); break;
+    case 102408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 1024, 8, CK, true, EXACT>), g, b, 0, st, p); break;
     default: {
       if (p.part) {
         hipLaunchKernelGGL((mxf::norm_bwd_cols_kernel<T, CK>), dim3((unsigned)((p.cols + 255) / 256), (unsigned)parts),
@@ -600,16 +624,16 @@ hipError_t launch_bwd(const NormParams& p, int parts, hipStream_t st) {
       }
       const dim3 rg((unsigned)(p.rows < 512 ? p.rows : 512));
       if (s.tpr)
-        hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, W, 1024, 16, CK, false>), rg, b, 0, st, p);
+        hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 1024, 16, CK, false, EXACT>), rg, b, 0, st, p);
       else
         hipLaunchKernelGGL((mxf::norm_bwd_long_kernel<T, CK>), rg, b, 0, st, p);
     }
   }
   return hipGetLastError();
 }
-template <class T, class W>
+template <class T, bool EXACT>
 hipError_t launch_bwd_any(const NormParams& p, int parts, hipStream_t st) {
-  return p.q ? launch_bwd<T, W, true>(p, parts, st) : launch_bwd<T, W, false>(p, parts, st);
+  return p.q ? launch_bwd<T, true, EXACT>(p, parts, st) : launch_bwd<T, false, EXACT>(p, parts, st);
 }
 
 }  // namespace
@@ -625,9 +649,9 @@ int mxf_norm_parts(int64_t rows, int64_t cols) {
 
 hipError_t mxf_launch_norm_fwd(const NormParams& p, bool f32, hipStream_t st) {
   if (f32)
-    p.w_f32 ? launch_fwd<float, float>(p, st) : launch_fwd<float, uint16_t>(p, st);
+    p.cols % 4 ? launch_fwd<float, false>(p, st) : launch_fwd<float, true>(p, st);
   else
-    p.w_f32 ? launch_fwd<uint16_t, float>(p, st) : launch_fwd<uint16_t, uint16_t>(p, st);
+    p.cols % 8 ? launch_fwd<uint16_t, false>(p, st) : launch_fwd<uint16_t, true>(p, st);
   return hipGetLastError();
 }
 
@@ -635,9 +659,9 @@ hipError_t mxf_launch_norm_fwd(const NormParams& p, bool f32, hipStream_t st) {
 hipError_t mxf_launch_norm_bwd(const NormParams& p, bool f32, hipStream_t st) {
   const int parts = mxf_norm_parts(p.rows, p.cols);
   if (p.rows > 0) {
-    hipError_t e = f32 ? (p.w_f32 ? launch_bwd_any<float, float>(p, parts, st) : launch_bwd_any<float, uint16_t>(p, parts, st))
-                       : (p.w_f32 ? launch_bwd_any<uint16_t, float>(p, parts, st)
-                                  : launch_bwd_any<uint16_t, uint16_t>(p, parts, st));
+    hipError_t e = f32 ? (p.cols % 4 ? launch_bwd_any<float, false>(p, parts, st) : launch_bwd_any<float, true>(p, parts, st))
+                       : (p.cols % 8 ? launch_bwd_any<uint16_t, false>(p, parts, st)
+                                     : launch_bwd_any<uint16_t, true>(p, parts, st));
     if (e != hipSuccess) return e;
   }
   if (!p.part) return hipSuccess;
