@@ -63,17 +63,21 @@ struct Elem<float> {
   }
 };
 
-// 16 bytes of a row as loaded, of which the first n elements exist (n >= VEC: all); the others are zero. EXACT:
-// rows end on a chunk, so n is all or none.
+// 16 bytes at column c of a row. EXACT (rows end on a chunk): a lane past the end loads column 0 instead, so
+// that the load needs no branch (after one the compiler cannot count the loads in flight and waits for all
+// of them), and is left out where the chunk is used. Else the elements that exist, and zeros.
 template <class T, bool EXACT>
-__device__ __forceinline__ u32x4_t load_chunk(const T* p, int n) {
+__device__ __forceinline__ u32x4_t load_chunk(const T* row, int c, int cols) {
   u32x4_t v = {0, 0, 0, 0};
-  if (EXACT ? n > 0 : n >= Elem<T>::VEC) {
-    __builtin_memcpy(&v, p, 16);
-  } else if (!EXACT && n > 0) {
+  const int n = cols - c;
+  if constexpr (EXACT) {
+    __builtin_memcpy(&v, row + (n > 0 ? c : 0), 16);
+  } else if (n >= Elem<T>::VEC) {
+    __builtin_memcpy(&v, row + c, 16);
+  } else if (n > 0) {
     uint32_t e[Elem<T>::VEC];
 #pragma unroll
-    for (int i = 0; i < Elem<T>::VEC; ++i) e[i] = i < n ? bits_of(p[i]) : 0u;
+    for (int i = 0; i < Elem<T>::VEC; ++i) e[i] = i < n ? bits_of(row[c + i]) : 0u;
     if constexpr (sizeof(T) == 4)
       v = (u32x4_t){e[0], e[1], e[2], e[3]};
     else
@@ -81,12 +85,15 @@ __device__ __forceinline__ u32x4_t load_chunk(const T* p, int n) {
   }
   return v;
 }
+
+// (past the caches' retention: y and dx are larger than the caches when it matters. 16384 x 2048 backward from
+// the checkpoint 36 against 39 us, 8192 x 7168 forward 66 against 69; loads gain nothing from it.)
+typedef u32x4_t u32x4_any __attribute__((aligned(1)));
 template <class T, bool EXACT>
 __device__ __forceinline__ void store_chunk(T* p, const float* f, int n) {
   constexpr int VEC = Elem<T>::VEC;
   if (EXACT ? n > 0 : n >= VEC) {
-    const u32x4_t v = Elem<T>::pack(f);
-    __builtin_memcpy(p, &v, 16);
+    __builtin_nontemporal_store(Elem<T>::pack(f), reinterpret_cast<u32x4_any*>(p));
   } else if (!EXACT) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
@@ -146,6 +153,12 @@ __device__ __forceinline__ float wave_sum(float v) {
   v = dpp_add<0x142, 0xA>(v);
   v = dpp_add<0x143, 0xC>(v);
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// s / n with the product's error taken out, so that a constant row's mean is exact (inv = 1 / n rounded).
+__device__ __forceinline__ float exact_mean(float s, float n, float inv) {
+  const float m = s * inv;
+  return fmaf(fmaf(-m, n, s), inv, m);
 }
 
 // Sum of a pair over the TPR threads of a row; a block of BLK threads holds BLK / TPR rows. TPR 64 is one
@@ -249,49 +262,50 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormPar
   __shared__ float2 red[2 * (BLK / 64)];
   int phase = 0;
   const int t = threadIdx.x % TPR, cols = (int)p.cols, G = (cols + 31) >> 5;
-  const float n = (float)cols;  // divided by, so that a constant row's mean is exact
+  const float n = (float)cols, inv = 1.0f / n;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  u32x4_t x[NC];  // the next row
-  auto fetch = [&](int64_t r) {
-    const T* src = reinterpret_cast<const T*>(p.x) + r * p.ldx;
+  if (TPR == 64 && row >= p.rows) return;
+  u32x4_t x0[NC], x1[NC];  // this row and the next, in turn
+  auto fetch = [&](int64_t r, u32x4_t* x) {  // (past the last row: the last)
+    const T* src = reinterpret_cast<const T*>(p.x) + (r < p.rows ? r : p.rows - 1) * p.ldx;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int c = (j * TPR + t) * VEC;
-      x[j] = load_chunk<T, EXACT>(src + c, cols - c);
-    }
+    for (int j = 0; j < NC; ++j) x[j] = load_chunk<T, EXACT>(src, (j * TPR + t) * VEC, cols);
   };
   float w[NE], b[NE];
-  if (row < p.rows) fetch(row);
+  fetch(row, x0);
+  fetch(row + step, x1);
   load_weights<VEC, TPR, NE>(p.w, p.w_f32, t, cols, 1.0f, w);
   load_weights<VEC, TPR, NE>(p.b, p.w_f32, t, cols, 0.0f, b);
-  for (; row < p.rows; row += step) {
+  auto one_row = [&](u32x4_t* x, u32x4_t* next) {
     float v[NE];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      if (EXACT && (j * TPR + t) * VEC >= cols) continue;
       Elem<T>::unpack(x[j], v + j * VEC);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) sum += v[j * VEC + i];
     }
-    if (row + step < p.rows) fetch(row + step);
-    const float mean = row_sum<TPR, BLK>(sum, red, phase) / n;
+    fetch(row + 2 * step, x);
+    const float mean = exact_mean(row_sum<TPR, BLK>(sum, red, phase), n, inv);
     float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int m = cols - (j * TPR + t) * VEC;
+      if (EXACT && m <= 0) continue;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         float& d = v[j * VEC + i];
-        d = (EXACT ? m > 0 : i < m) ? d - mean : 0.0f;
+        d = EXACT || i < m ? d - mean : 0.0f;
         ss += d * d;
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR, BLK>(ss, red, phase) / n + p.eps);
+    const float rstd = rsqrtf(row_sum<TPR, BLK>(ss, red, phase) * inv + p.eps);
     // The next row's loads end here, before this row's stores are issued: loads and stores are counted in
     // order, so a wait for the loads after them would wait for the stores as well.
 #pragma unroll
-    for (int j = 0; j < NC; ++j) asm volatile("" : "+v"(x[j]));
+    for (int j = 0; j < NC; ++j) asm volatile("" : "+v"(next[j]));
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
@@ -300,6 +314,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormPar
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * TPR + t) * VEC;
+      if (EXACT && c >= cols) continue;
       float o[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
@@ -308,10 +323,17 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormPar
         o[i] = xh * w[j * VEC + i] + b[j * VEC + i];
       }
       store_chunk<T, EXACT>(y + c, o, cols - c);
-      // a lane past the end still takes part in its group's maximum; its xh is NaN in a row whose rstd
-      // is, as is every other of that row
+      // (EXACT: a lane that is left out counts as 0 in its group's maximum; else a lane past the end takes
+      // part with zeros, or with NaN in a row whose rstd is, as is every other of that row)
       if (p.q) put_codes<VEC, EXACT>(v + j * VEC, cols - c, c, p.q + row * cols, p.s + row * G);
     }
+    row += step;
+  };
+#pragma unroll
+  for (int j = 0; j < NC; ++j) asm volatile("" : "+v"(x0[j]));
+  while (row < p.rows) {
+    one_row(x0, x1);
+    if (row < p.rows) one_row(x1, x0);
   }
 }
 
@@ -322,19 +344,19 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormParams p) {
   __shared__ float2 red[32];
   int phase = 0;
   const int t = threadIdx.x, cols = (int)p.cols, G = (cols + 31) >> 5;
-  const float n = (float)cols;
+  const float n = (float)cols, inv = 1.0f / n;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx;
     T* y = reinterpret_cast<T*>(p.y) + row * p.ldy;
     float sum = 0.0f;
     for (int c = t; c < cols; c += 1024) sum += Elem<T>::get(x[c]);
-    const float mean = row_sum<1024, 1024>(sum, red, phase) / n;
+    const float mean = exact_mean(row_sum<1024, 1024>(sum, red, phase), n, inv);
     float ss = 0.0f;
     for (int c = t; c < cols; c += 1024) {
       const float d = Elem<T>::get(x[c]) - mean;
       ss += d * d;
     }
-    const float rstd = 1.0f / sqrtf(row_sum<1024, 1024>(ss, red, phase) / n + p.eps);
+    const float rstd = rsqrtf(row_sum<1024, 1024>(ss, red, phase) * inv + p.eps);
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
@@ -360,97 +382,116 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
   __shared__ float2 red[2 * (BLK / 64)];
   int phase = 0;
   const int t = threadIdx.x % TPR, cols = (int)p.cols, G = (cols + 31) >> 5;
-  const float n = (float)cols;
+  const float inv = 1.0f / (float)cols;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row0 = (int64_t)blockIdx.x * RPB;  // the block's first row; all its threads walk together
   const int sub = threadIdx.x / TPR;
-  // the next row: dy, x or its codes and scales, mean, rstd
-  u32x4_t dyv[NC], xv[CK ? 1 : NC];
-  uint32_t kv[CK ? NC : 1][VEC / 4], sv[CK ? NC : 1];
-  float mean = 0.0f, rstd = 0.0f;
-  auto fetch = [&](int64_t r) {
+  struct Row {  // dy, x or its codes and scales, mean, rstd
+    u32x4_t dy[NC], x[CK ? 1 : NC];
+    uint32_t k[CK ? NC : 1][VEC / 4], s[CK ? NC : 1];
+    float mean, rstd;
+  };
+  Row r0, r1;  // this row and the next, in turn
+  auto fetch = [&](int64_t r, Row& o) {
+    r = r < p.rows ? r : p.rows - 1;
     const T* dy = reinterpret_cast<const T*>(p.dy) + r * p.ldy;
     const T* x = CK ? nullptr : reinterpret_cast<const T*>(p.x) + r * p.ldx;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * TPR + t) * VEC, m = cols - c;
-      dyv[j] = load_chunk<T, EXACT>(dy + c, m);
+      o.dy[j] = load_chunk<T, EXACT>(dy, c, cols);
       if constexpr (CK) {
-        const uint8_t* q = p.q + r * cols + c;
+        const uint8_t* q = p.q + r * cols;
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) kv[j][i] = 0;
-        if (EXACT ? m > 0 : m >= VEC) {
-          __builtin_memcpy(kv[j], q, VEC);
-        } else if (!EXACT) {
+        for (int i = 0; i < VEC / 4; ++i) o.k[j][i] = 0;
+        if constexpr (EXACT) {
+          __builtin_memcpy(o.k[j], q + (m > 0 ? c : 0), VEC);
+        } else if (m >= VEC) {
+          __builtin_memcpy(o.k[j], q + c, VEC);
+        } else {
 #pragma unroll
           for (int i = 0; i < VEC; ++i)
-            if (i < m) kv[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
+            if (i < m) o.k[j][i / 4] |= (uint32_t)q[c + i] << (8 * (i % 4));
         }
-        sv[j] = m > 0 ? p.s[r * G + (c >> 5)] : 0u;
+        o.s[j] = p.s[r * G + (m > 0 ? c >> 5 : 0)];
       } else {
-        xv[j] = load_chunk<T, EXACT>(x + c, m);
+        o.x[j] = load_chunk<T, EXACT>(x, c, cols);
       }
     }
-    if (!CK) mean = p.mean[r];
-    rstd = p.rstd[r];
+    o.mean = CK ? 0.0f : p.mean[r];
+    o.rstd = p.rstd[r];
   };
   float w[NE], dw[SUMS ? NE : 1], db[SUMS ? NE : 1];
-  if (row0 + sub < p.rows) fetch(row0 + sub);
+  fetch(row0 + sub, r0);
+  fetch(row0 + sub + step, r1);
   load_weights<VEC, TPR, NE>(p.w, p.w_f32, t, cols, 1.0f, w);
 #pragma unroll
   for (int i = 0; i < (SUMS ? NE : 1); ++i) dw[i] = db[i] = 0.0f;
-  for (; row0 < p.rows; row0 += step) {
+  auto one_row = [&](Row& r, Row& next) {
     const int64_t row = row0 + sub;
-    const bool on = row < p.rows;  // (whole wavefronts)
+    const bool on = row < p.rows;  // (whole wavefronts; the others hold the last row again and drop it)
     float g[NE], xh[NE];
     float c1 = 0.0f, c2 = 0.0f;
-    const float rs = rstd;
-    if (on) {  // (elements past the row's end have dy = 0 and add nothing)
+    const float rs = r.rstd;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        float xf[VEC];
-        Elem<T>::unpack(dyv[j], g + j * VEC);
-        if (!CK) Elem<T>::unpack(xv[CK ? 0 : j], xf);
-        const float sc = CK ? ckpt_scale(sv[j]) : 0.0f;
+    for (int j = 0; j < NC; ++j) {  // (elements past the row's end have dy = 0 and add nothing)
+      if (!on || (EXACT && (j * TPR + t) * VEC >= cols)) continue;
+      float xf[VEC];
+      Elem<T>::unpack(r.dy[j], g + j * VEC);
+      if (!CK) Elem<T>::unpack(r.x[CK ? 0 : j], xf);
+      const float sc = CK ? ckpt_scale(r.s[j]) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int k = j * VEC + i;
-          xh[k] = CK ? ckpt_value(kv[j], i, sc) : (xf[i] - mean) * rs;
-          if constexpr (SUMS) {
-            dw[k] += g[k] * xh[k];
-            db[k] += g[k];
-          }
-          g[k] *= w[k];
-          c1 += g[k];
-          c2 += g[k] * xh[k];
+      for (int i = 0; i < VEC; ++i) {
+        const int k = j * VEC + i;
+        xh[k] = CK ? ckpt_value(r.k[j], i, sc) : (xf[i] - r.mean) * rs;
+        if constexpr (SUMS) {
+          dw[k] += g[k] * xh[k];
+          db[k] += g[k];
         }
+        g[k] *= w[k];
+        c1 += g[k];
+        c2 += g[k] * xh[k];
       }
     }
-    if (row + step < p.rows) fetch(row + step);
+    fetch(row + 2 * step, r);
     row_sum2<TPR, BLK>(c1, c2, red, phase);
-    c1 /= n;
-    c2 /= n;
+    c1 *= inv;
+    c2 *= inv;
     // (the next row's loads end before this row's stores are issued, as in the forward)
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      asm volatile("" : "+v"(dyv[j]));
+      asm volatile("" : "+v"(next.dy[j]));
       if constexpr (CK) {
-        asm volatile("" : "+v"(kv[j][0]), "+v"(sv[j]));
-        if constexpr (VEC == 8) asm volatile("" : "+v"(kv[j][1]));
+        asm volatile("" : "+v"(next.k[j][0]), "+v"(next.s[j]));
+        if constexpr (VEC == 8) asm volatile("" : "+v"(next.k[j][1]));
       } else {
-        asm volatile("" : "+v"(xv[j]));
+        asm volatile("" : "+v"(next.x[j]));
       }
     }
-    if (!on) continue;
+    row0 += step;
+    if (!on) return;
     T* dx = reinterpret_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * TPR + t) * VEC;
+      if (EXACT && c >= cols) continue;
       float o[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) o[i] = rs * (g[j * VEC + i] - c1 - xh[j * VEC + i] * c2);
       store_chunk<T, EXACT>(dx + c, o, cols - c);
     }
+  };
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    asm volatile("" : "+v"(r0.dy[j]));
+    if constexpr (CK)
+      asm volatile("" : "+v"(r0.k[j][0]), "+v"(r0.k[j][VEC / 4 - 1]), "+v"(r0.s[j]));
+    else
+      asm volatile("" : "+v"(r0.x[j]));
+  }
+  while (row0 < p.rows) {
+    one_row(r0, r1);
+    if (row0 < p.rows) one_row(r1, r0);
   }
   if constexpr (SUMS) {
     if (!p.part) return;
@@ -578,19 +619,19 @@ struct NormShape {
 // Eight elements per thread up to 8192 columns: the next row's loads in flight and enough wavefronts per CU;
 // with 32 per thread (a wavefront per row of 2048, no barrier) the registers left two wavefronts per
 // SIMD and the forward measured TODO.
-NormShape norm_shape(int64_t cols) {
+NormShape norm_shape(int64_t cols, bool f32) {
   if (cols <= 512) return {64, 8};
   if (cols <= 1024) return {128, 8};
   if (cols <= 2048) return {256, 8};
   if (cols <= 4096) return {512, 8};
   if (cols <= 8192) return {1024, 8};
-  if (cols <= 16384) return {1024, 16};
+  if (cols <= 16384 && !f32) return {1024, 16};  // (FP32: a row and the next no longer fit)
   return {0, 0};
 }
 
 template <class T, bool EXACT>
 void launch_fwd(const NormParams& p, hipStream_t st) {
-  NormShape s = norm_shape(p.cols);
+  NormShape s = norm_shape(p.cols, sizeof(T) == 4);
   if (s.tpr == 128) s.tpr = 256;  // one row per block, half of its lanes idle at most
   const int blk = s.tpr > 256 ? s.tpr : s.tpr ? 256 : 1024;
   const int64_t rpb = s.tpr == 64 ? 4 : 1, need = (p.rows + rpb - 1) / rpb, most = 256 * 2048 / blk;
@@ -600,14 +641,16 @@ void launch_fwd(const NormParams& p, hipStream_t st) {
     case 25608: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 256, 8, EXACT>), g, b, 0, st, p); break;
     case 51208: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 512, 8, EXACT>), g, b, 0, st, p); break;
     case 102408: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 1024, 8, EXACT>), g, b, 0, st, p); break;
-    case 102416: hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 1024, 16, EXACT>), g, b, 0, st, p); break;
+    case 102416:
+      if constexpr (sizeof(T) == 2) hipLaunchKernelGGL((mxf::norm_fwd_kernel<T, 1024, 16, EXACT>), g, b, 0, st, p);
+      break;
     default: hipLaunchKernelGGL((mxf::norm_fwd_long_kernel<T>), g, b, 0, st, p);
   }
 }
 
 template <class T, bool CK, bool EXACT>
 hipError_t launch_bwd(const NormParams& p, int parts, hipStream_t st) {
-  const NormShape s = norm_shape(p.cols);
+  const NormShape s = norm_shape(p.cols, sizeof(T) == 4);
   const dim3 g((unsigned)parts), b(1024);
   switch (s.key()) {
     case 6408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 64, 8, CK, true, EXACT>), g, b, 0, st, p); break;
@@ -623,10 +666,13 @@ hipError_t launch_bwd(const NormParams& p, int parts, hipStream_t st) {
         if (e != hipSuccess) return e;
       }
       const dim3 rg((unsigned)(p.rows < 512 ? p.rows : 512));
-      if (s.tpr)
-        hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 1024, 16, CK, false, EXACT>), rg, b, 0, st, p);
-      else
-        hipLaunchKernelGGL((mxf::norm_bwd_long_kernel<T, CK>), rg, b, 0, st, p);
+      if constexpr (sizeof(T) == 2) {
+        if (s.tpr) {
+          hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 1024, 16, CK, false, EXACT>), rg, b, 0, st, p);
+          break;
+        }
+      }
+      hipLaunchKernelGGL((mxf::norm_bwd_long_kernel<T, CK>), rg, b, 0, st, p);
     }
   }
   return hipGetLastError();
@@ -640,7 +686,7 @@ hipError_t launch_bwd_any(const NormParams& p, int parts, hipStream_t st) {
 
 // Blocks of the backward, which is also the number of partial rows.
 int mxf_norm_parts(int64_t rows, int64_t cols) {
-  const NormShape s = norm_shape(cols);
+  const NormShape s = norm_shape(cols, false);
   const bool one = s.ne == 8;  // dx and the column sums in one kernel
   const int64_t need = one ? (rows + 1024 / s.tpr - 1) / (1024 / s.tpr) : rows;
   const int64_t most = one ? 256 : 128;
