@@ -59,6 +59,23 @@ def _stream_of(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(name, *args):
+    """One library call (looked up once), its status checked."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(_abi.lib(), name)
+    status = fn(*args)
+    if status:
+        _abi._check(status)
+
+
+_entry = {}
+
+
 def _on_stream(fn):
     """Adds ``stream=``: the call runs, and allocates, with that stream as the current one."""
     @functools.wraps(fn)
@@ -101,8 +118,8 @@ def _norm_fwd(x, weight, bias, eps, stats, ckpt):
     rstd = torch.empty(rows, dtype=torch.float32, device=dev) if stats or ckpt else None
     q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if ckpt else None
     s = torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=dev) if ckpt else None
-    _abi.mxf_layer_norm_fwd(NormDesc(rows, cols, ld, cols, cols, eps, flags), x, weight, bias, y, mean, rstd, q, s,
-                            _stream_of(dev))
+    _run("mxf_layer_norm_fwd", NormDesc(rows, cols, ld, cols, cols, eps, flags), x.data_ptr(), _ptr(weight),
+         _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(q), _ptr(s), _stream_of(dev))
     return y, mean, rstd, q, s
 
 
@@ -142,8 +159,10 @@ def _norm_bwd(dy, x, q, s, mean, rstd, weight):
     dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
     dw = torch.empty((2, cols), dtype=torch.float32, device=dev)
     ws = torch.empty(_abi.layer_norm_workspace_bytes(desc), dtype=torch.uint8, device=dev)
-    _abi.mxf_layer_norm_bwd(desc, dy, x, q, s, mean, rstd, weight, dx, dw[0], dw[1], ws, _stream_of(dev))
-    return dx, dw[0], dw[1]
+    dw, db = dw.unbind(0)
+    _run("mxf_layer_norm_bwd", desc, dy.data_ptr(), _ptr(x), _ptr(q), _ptr(s), _ptr(mean), rstd.data_ptr(),
+         _ptr(weight), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(), _stream_of(dev))
+    return dx, dw, db
 
 
 @_on_stream
@@ -174,7 +193,8 @@ def swiglu_ckpt_fwd(gu):
     h = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
     q = torch.empty((2 * rows, F), dtype=torch.uint8, device=dev)
     s = torch.empty((2 * rows, (F + 31) // 32), dtype=torch.uint8, device=dev)
-    _abi.mxf_swiglu_ckpt_fwd(gu, rows, F, ld, h, F, q, s, _stream_of(dev))
+    _run("mxf_swiglu_ckpt_fwd", gu.data_ptr(), rows, F, ld, h.data_ptr(), F, q.data_ptr(), s.data_ptr(),
+         _stream_of(dev))
     return h, q, s
 
 
@@ -191,7 +211,8 @@ def swiglu_ckpt_bwd(dh, q, s, recompute=True):
     _dense(s, (2 * rows, (F + 31) // 32), torch.uint8, dev, "s")
     dgu = torch.empty((rows, 2 * F), dtype=torch.bfloat16, device=dev)
     h = torch.empty((rows, F), dtype=torch.bfloat16, device=dev) if recompute else None
-    _abi.mxf_swiglu_ckpt_bwd(dh, ld, q, s, rows, F, dgu, 2 * F, h, F, _stream_of(dev))
+    _run("mxf_swiglu_ckpt_bwd", dh.data_ptr(), ld, q.data_ptr(), s.data_ptr(), rows, F, dgu.data_ptr(), 2 * F,
+         _ptr(h), F, _stream_of(dev))
     return dgu, h
 
 
@@ -225,8 +246,8 @@ def grouped_gemm_fwd(x, w, offs, out_dtype=None, status=None):
     flags = _grouped_args(w.shape, offs, x.device, out_dtype, status)
     E, N, _ = w.shape
     y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    _abi.mxf_grouped_gemm_fwd(GroupedDesc(E, flags, M, N, K, ld, N), offs, x, w, y, status,
-                              _stream_of(x.device))
+    _run("grouped_gemm_fwd", GroupedDesc(E, flags, M, N, K, ld, N), offs.data_ptr(), x.data_ptr(), w.data_ptr(),
+         y.data_ptr(), _ptr(status), _stream_of(x.device))
     return y
 
 
@@ -244,8 +265,8 @@ def grouped_gemm_dgrad(dy, w, offs, out_dtype=None, status=None):
     flags = _grouped_args(w.shape, offs, dy.device, out_dtype, status)
     E, _, K = w.shape
     dx = torch.empty((M, K), dtype=out_dtype, device=dy.device)
-    _abi.mxf_grouped_gemm_dgrad(GroupedDesc(E, flags, M, N, K, K, ld), offs, dy, w, dx, status,
-                                _stream_of(dy.device))
+    _run("grouped_gemm_dgrad", GroupedDesc(E, flags, M, N, K, K, ld), offs.data_ptr(), dy.data_ptr(), w.data_ptr(),
+         dx.data_ptr(), _ptr(status), _stream_of(dy.device))
     return dx
 
 
@@ -286,7 +307,7 @@ def grouped_gemm_wgrad(dy, x, offs, out_dtype=None, accumulate=None, status=None
     flags = _grouped_args((E,), offs, dy.device, out_dtype, status)
     if accumulate is not None:
         flags |= _abi.GROUPED_ACCUM
-    _abi.mxf_grouped_gemm_wgrad(GroupedDesc(E, flags, M, N, K, ldx, ldy), offs, dy, x, q, s, dw, status,
-                                _stream_of(dy.device))
+    _run("grouped_gemm_wgrad", GroupedDesc(E, flags, M, N, K, ldx, ldy), offs.data_ptr(), dy.data_ptr(), _ptr(x),
+         _ptr(q), _ptr(s), dw.data_ptr(), _ptr(status), _stream_of(dy.device))
     return dw
 
