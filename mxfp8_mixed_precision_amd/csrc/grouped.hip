@@ -213,73 +213,111 @@ __device__ __forceinline__ uint32_t bf16_of_fp8(uint32_t w, bool hi, float scale
                                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
 }
 
+// v >> bits (bits < 128, per lane) of a 128-bit value.
+__device__ __forceinline__ u32x4_t shr128(u32x4_t v, uint32_t bits) {
+  const uint32_t b = bits & 31;
+  u32x4_t r = {__builtin_amdgcn_alignbit(v[1], v[0], b), __builtin_amdgcn_alignbit(v[2], v[1], b),
+               __builtin_amdgcn_alignbit(v[3], v[2], b), v[3] >> b};
+  if (bits & 32) r = (u32x4_t){r[1], r[2], r[3], 0};
+  if (bits & 64) r = (u32x4_t){r[2], r[3], 0, 0};
+  return r;
+}
+
 // An operand that passes through registers: BF16 at any alignment, or (X8, contraction-slow) codes with
 // their scales. LDS layout and reads are Operand's.
+//
+// A fetch is 16 bytes of a row. The one in which a row ends is loaded from its end backwards (into elements
+// that its neighbour holds) and shifted when it is used, and a lane with nothing to fetch loads the tile's
+// first piece and drops it: no branch between the loads. Rows shorter than a fetch go element by element.
 template <bool KC, int R, bool X8>
 struct StagedOperand : Operand<KC, R> {
   using Base = Operand<KC, R>;
   static constexpr int PER = X8 ? 16 : 8;            // elements per fetch
+  static constexpr int BITS = 128 / PER;             // and of an element
   static constexpr int NF = R * 64 / PER / 256;      // fetches per thread and stage
   static constexpr int PPR = (KC ? 64 : R) / PER;    // fetches per row
+  static constexpr int RPT = 256 / PPR;              // rows per round of the block's fetches
   const uint8_t* src;   // the tile's first element of the stage to fetch next
   const uint8_t* scl;   // X8: its row's first scale of this tile
   int64_t ldb, lds_;    // bytes between rows, scales between rows
   int valid;
+  bool tiny;            // rows of fewer than PER elements
   u32x4_t v[NF];
   uint32_t sc[X8 ? NF : 1];
+  uint32_t have, shift;  // of the fetch in registers: which pieces exist, bits to drop
 
   __device__ __forceinline__ void init(const void* origin, const uint8_t* scales, int64_t ld, int64_t ld_scales,
-                                       int valid_, int w0, uint32_t lds) {
+                                       int64_t row_length, int valid_, int w0, uint32_t lds) {
     Base::init_reads(w0, lds);
     src = reinterpret_cast<const uint8_t*>(origin);
     scl = scales;
     ldb = X8 ? ld : 2 * ld;
     lds_ = ld_scales;
     valid = valid_;
+    tiny = row_length < PER;
   }
   __device__ __forceinline__ void fetch(int left) {
+    const int r0 = (int)threadIdx.x / PPR, c = (int)threadIdx.x % PPR * PER;
+    const int rows = KC ? valid : left, width = KC ? left : valid;  // that exist
+    have = 0;
+    shift = 0;
+    if (tiny) {
 #pragma unroll
-    for (int t = 0; t < NF; ++t) {
-      const int id = t * 256 + (int)threadIdx.x, r = id / PPR, c = id % PPR * PER;
-      const int n = min(PER, KC ? (r < valid ? left - c : 0) : (r < left ? valid - c : 0));
-      const uint8_t* p = src + r * ldb + (X8 ? c : 2 * c);
-      v[t] = (u32x4_t){0, 0, 0, 0};
-      if (X8) sc[t] = n > 0 ? scl[r * lds_ + (c >> 5)] : 0u;
-      if (n == PER) {
-        v[t] = load16_any(p);
-      } else if (n > 0) {
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          const uint32_t x = e < n ? (X8 ? (uint32_t)p[e] : (uint32_t) reinterpret_cast<const uint16_t*>(p)[e]) : 0u;
-          if (X8)
-            v[t][e / 4] |= x << (8 * (e % 4));
-          else
-            v[t][e / 2] |= x << (16 * (e % 2));
+      for (int t = 0; t < NF; ++t) {
+        const int r = r0 + t * RPT;
+        const uint8_t* p = src + r * ldb;
+        v[t] = (u32x4_t){0, 0, 0, 0};
+        if (X8) sc[t] = r < rows && c < width ? scl[r * lds_ + (c >> 5)] : 0u;
+#pragma unroll 1
+        for (int e = 0; e < PER; ++e) {  // the next element enters at the top
+          uint32_t x = 0;
+          if (r < rows && c + e < width) x = X8 ? p[c + e] : reinterpret_cast<const uint16_t*>(p)[c + e];
+          v[t] = shr128(v[t], BITS);
+          v[t][3] |= x << (32 - BITS);
         }
+      }
+      have = (1u << NF) - 1;
+    } else if (rows > 0 && width > 0) {
+      const int cc = c < width ? c : 0, back = max(0, PER - (width - cc));
+      shift = (uint32_t)(back * BITS);
+      const uint8_t* p = src + (X8 ? cc - back : 2 * (cc - back));
+#pragma unroll
+      for (int t = 0; t < NF; ++t) {
+        const int r = r0 + t * RPT, rr = r < rows ? r : 0;
+        v[t] = load16_any(p + rr * ldb);
+        if (X8) sc[t] = scl[rr * lds_ + (cc >> 5)];
+        have |= (r < rows && c < width ? 1u : 0u) << t;
       }
     }
     src += KC ? 128 : 64 * ldb;
     if (X8) scl += 64 * lds_;
   }
   __device__ __forceinline__ void put(uint8_t* unit) const {
+    const int r0 = (int)threadIdx.x / PPR, c = (int)threadIdx.x % PPR * (PER / 8);  // row, 16-byte chunk
+    const bool cut = __any(shift != 0);
 #pragma unroll
     for (int t = 0; t < NF; ++t) {
-      const int id = t * 256 + (int)threadIdx.x, r = id / PPR, c = id % PPR * PER / 8;  // row, 16-byte chunk
+      const int r = r0 + t * RPT;
+      u32x4_t x = v[t];
+      if (cut) x = shr128(x, shift);
+      const bool in = (have >> t) & 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = in ? x[i] : 0u;
       uint8_t* row = unit + r * (KC ? 128 : R * 2);
       if constexpr (X8) {
-        const float s = e8m0_value(sc[t]);
+        const float s = e8m0_value(in ? sc[t] : 0u);
         u32x4_t lo, hi;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          lo[2 * i] = bf16_of_fp8(v[t][i], false, s);
-          lo[2 * i + 1] = bf16_of_fp8(v[t][i], true, s);
-          hi[2 * i] = bf16_of_fp8(v[t][2 + i], false, s);
-          hi[2 * i + 1] = bf16_of_fp8(v[t][2 + i], true, s);
+          lo[2 * i] = bf16_of_fp8(x[i], false, s);
+          lo[2 * i + 1] = bf16_of_fp8(x[i], true, s);
+          hi[2 * i] = bf16_of_fp8(x[2 + i], false, s);
+          hi[2 * i + 1] = bf16_of_fp8(x[2 + i], true, s);
         }
         *reinterpret_cast<u32x4_t*>(row + ((c ^ (4 * (r & 3))) << 4)) = lo;
         *reinterpret_cast<u32x4_t*>(row + (((c + 1) ^ (4 * (r & 3))) << 4)) = hi;
       } else {
-        *reinterpret_cast<u32x4_t*>(row + ((c ^ (KC ? (r >> 1) & 7 : 4 * (r & 3))) << 4)) = v[t];
+        *reinterpret_cast<u32x4_t*>(row + ((c ^ (KC ? (r >> 1) & 7 : 4 * (r & 3))) << 4)) = x;
       }
     }
   }
@@ -324,11 +362,11 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   OA oa;
   OB ob;
   if constexpr (SA)
-    oa.init(a, nullptr, p.lda, 0, mr, wm * (BM / 2), lds0);
+    oa.init(a, nullptr, p.lda, 0, OP == 0 ? p.K : p.N, mr, wm * (BM / 2), lds0);
   else
     oa.init(a, p.lda, mr, wid, wm * (BM / 2), lds0);
   if constexpr (SB)
-    ob.init(b, b_scales, ldb, (p.K + 31) / 32, nc, wn * (BN / 2), lds0);
+    ob.init(b, b_scales, ldb, (p.K + 31) / 32, p.K, nc, wn * (BN / 2), lds0);
   else
     ob.init(reinterpret_cast<const uint16_t*>(b), ldb, nc, wid, wn * (BN / 2), lds0);
   constexpr int NLA = SA ? 0 : OA::NLOAD, NLB = SB ? 0 : OB::NLOAD;  // direct loads of a unit per wavefront
