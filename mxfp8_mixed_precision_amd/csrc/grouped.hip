@@ -352,10 +352,11 @@ struct CodesOperand : Operand<false, R> {
     const bool in = c * 16 < valid;
     voff = in ? (uint32_t)r0 * ldb + c * 16 : kNoElement;
     soff = in ? (uint32_t)r0 * lds_ + (c >> 1) : kNoElement;
-    // a lane's two 16-byte halves go in two writes; lanes 8-15 of 16 write the upper half first, so that the
-    // 16 lanes of a write hit different bank groups
-    put0 = r0 * (R * 2) + (((2 * c + ((c >> 3) & 1)) ^ (4 * (r0 & 3))) << 4);
+    // a lane's two 16-byte halves go in two writes; lanes 4-11 of 16 write the upper half first, so that 8 and 16
+    // neighbouring lanes of a write hit different bank groups
+    put0 = r0 * (R * 2) + (((2 * c + upper()) ^ (4 * (r0 & 3))) << 4);
   }
+  static __device__ __forceinline__ int upper() { return ((threadIdx.x >> 2) ^ (threadIdx.x >> 3)) & 1; }
   __device__ __forceinline__ void begin(int l) { left = l; }
   __device__ __forceinline__ void piece(int t) {
     const __amdgpu_buffer_rsrc_t q = __builtin_amdgcn_make_buffer_rsrc((void*)src, 0, kNoElement, 0x00020000);
@@ -376,7 +377,7 @@ struct CodesOperand : Operand<false, R> {
   }
   __device__ __forceinline__ void put(uint8_t* unit, int t) const {
     const float s = e8m0_value(sc[t]);
-    const bool up = (threadIdx.x & 8) != 0;  // (PPR is 8 or 16: bit 3 of the piece's column, or of its row)
+    const bool up = upper();
     u32x4_t lo, hi, a, b;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -387,8 +388,8 @@ struct CodesOperand : Operand<false, R> {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      a[i] = PPR == 16 && up ? hi[i] : lo[i];
-      b[i] = PPR == 16 && up ? lo[i] : hi[i];
+      a[i] = up ? hi[i] : lo[i];
+      b[i] = up ? lo[i] : hi[i];
     }
     // (RPT rows further r % 4 is the same)
     *reinterpret_cast<u32x4_t*>(unit + put0 + t * RPT * (R * 2)) = a;
