@@ -731,19 +731,22 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_dw_kernel(Grou
   if (!ok) return;
   const uint32_t per = (uint32_t)row_tiles * (uint32_t)col_tiles;
   const int place = (int)(blockIdx.x / per);
-  int e = place;
+  int e = __builtin_amdgcn_readfirstlane(place), c0, c1;
   if (p.E <= 64) {
     const int lane = threadIdx.x & 63;
-    const int n = lane < p.E ? p.offs[lane + 1] - p.offs[lane] : -1;
+    const int lo = lane < p.E ? p.offs[lane] : 0, hi = lane < p.E ? p.offs[lane + 1] : -1, n = hi - lo;
     int rank = 0;
     for (int j = 0; j < p.E; ++j) {
       const int nj = __builtin_amdgcn_readlane(n, j);
       rank += nj > n || (nj == n && j < lane);
     }
-    e = __ffsll((unsigned long long)__ballot(lane < p.E && rank == place)) - 1;
+    e = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(lane < p.E && rank == place)) - 1);
+    c0 = __builtin_amdgcn_readlane(lo, e);
+    c1 = __builtin_amdgcn_readlane(hi, e);
+  } else {
+    c0 = p.offs[e];
+    c1 = p.offs[e + 1];
   }
-  e = __builtin_amdgcn_readfirstlane(e);
-  const int c0 = p.offs[e], c1 = p.offs[e + 1];
   const uint32_t pos = xcd_run(blockIdx.x % per, per);
   // (row tiles in groups, as above)
   constexpr uint32_t GM = 4;
@@ -803,8 +806,11 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
   const bool aligned = p.N % 8 == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && (p.bq || p.ldb % 8 == 0) &&
                        p.ldc % (p.out_f32 ? 4 : 8) == 0 && a16(p.a) && a16(p.b) && a16(p.c) && p.lda < (1 << 22) &&
                        p.ldb < (1 << 22);
-  // 256 x 256 tiles where they fill the chip
-  const bool big = (op == 2 ? p.E * ((om + 255) / 256) : (om + 255) / 256) * ((on + 255) / 256) >= ncu;
+  // 256 x 256 tiles where they fill the chip (forward of 24576 x 2816 x 2048, 64 experts: 335 us against 390 on
+  // 128 x 128; 4096 rows, 16 experts, too few: 72 against 65); in the weight gradient twice over, since the
+  // experts' tiles differ in length (8192 rows of 4 experts, 2048 x 2048, 256 tiles: 126 against 73).
+  const bool big = op == 2 ? p.E * ((om + 255) / 256) * ((on + 255) / 256) >= 2 * ncu
+                           : (om + 255) / 256 * ((on + 255) / 256) >= ncu;
   if (op == 0)
     return aligned ? launch_tiles<0, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<0, STAGED, STAGED>(p, big, ncu, st);
   if (op == 1)
