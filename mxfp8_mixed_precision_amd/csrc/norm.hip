@@ -86,6 +86,23 @@ __device__ __forceinline__ float exact_mean(float s, float n, float inv) {
   return fmaf(fmaf(-m, n, s), inv, m);
 }
 
+// Sum of NW wavefronts' values v[0..NW).
+template <int NW>
+__device__ __forceinline__ float2 waves_sum2(const float2* v) {
+  if constexpr ((NW & (NW - 1)) == 0) {
+    const float2 u = v[threadIdx.x & (NW - 1)];
+    return make_float2(lanes_sum<NW>(u.x), lanes_sum<NW>(u.y));
+  } else {
+    float2 s = v[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) {
+      s.x += v[i].x;
+      s.y += v[i].y;
+    }
+    return s;
+  }
+}
+
 // Sum of a pair over the TPR threads of a row; a block of BLK threads holds BLK / TPR rows. TPR 64 is one
 // wavefront; more takes one barrier of the block: the slots alternate, so the next call's writes
 // cannot meet this call's reads. `red`: 2 * BLK / 64 slots.
@@ -99,9 +116,9 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float2* red, int& p
     phase ^= 1;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = make_float2(a, b);
     __syncthreads();
-    const float2 v = slot[threadIdx.x / TPR * NW + (threadIdx.x & (NW - 1))];
-    a = lanes_sum<NW>(v.x);
-    b = lanes_sum<NW>(v.y);
+    const float2 v = waves_sum2<NW>(slot + threadIdx.x / TPR * NW);
+    a = v.x;
+    b = v.y;
   }
 }
 template <int TPR, int BLK>
@@ -284,12 +301,12 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormParams p) {
 
 // ------------------------------------------------------------------ backward
 
-// One pass: dx, and (SUMS) this block's partial dw and db in row blockIdx.x of the workspace. Blocks of 1024
+// One pass: dx, and (SUMS) this block's partial dw and db in row blockIdx.x of the workspace. Blocks of up to 1024
 // threads hold 1024 / TPR rows, so that one block per CU keeps enough loads in flight and leaves one partial
 // row: 256 partial rows cost 1/32 of the traffic of 8192 rows.
 template <class T, int TPR, int NE, bool CK, bool SUMS, bool EXACT>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p) {
-  constexpr int BLK = 1024, RPB = BLK / TPR;
+__global__ __launch_bounds__(1024 / TPR * TPR) void norm_bwd_kernel(NormParams p) {
+  constexpr int RPB = 1024 / TPR, BLK = RPB * TPR;
   constexpr int VEC = Elem<T>::VEC, NC = NE / VEC;
   __shared__ float2 red[2 * (BLK / 64)];
   int phase = 0;
@@ -541,6 +558,18 @@ NormShape norm_shape(int64_t cols, bool f32) {
   return {0, 0};
 }
 
+// In the backward a row's idle lanes hold a block's registers and loads: widths between powers of two have
+// shapes of their own (8192 BF16 rows with a checkpoint, 2560 columns: 30.2 us in 512 threads, 24.2 in 320;
+// 2816: 31.3, 26.5 in 384; 1411: 31.1, 28.4 in 192; 5120: 46.2 in 1024, 46.5 in 640, not kept). In the forward, with
+// a row per block, they gained nothing (2560: 20.9, 20.4; 5120: 35.6, 41.2).
+NormShape bwd_shape(int64_t cols, bool f32) {
+  NormShape s = norm_shape(cols, f32);
+  if (s.ne == 8)
+    for (int tpr : {192, 320, 384})
+      if (cols <= tpr * 8 && tpr < s.tpr) return {tpr, 8};
+  return s;
+}
+
 template <class T, bool EXACT>
 void launch_fwd(const NormParams& p, hipStream_t st) {
   NormShape s = norm_shape(p.cols, sizeof(T) == 4);
@@ -562,12 +591,15 @@ void launch_fwd(const NormParams& p, hipStream_t st) {
 
 template <class T, bool CK, bool EXACT>
 hipError_t launch_bwd(const NormParams& p, int parts, hipStream_t st) {
-  const NormShape s = norm_shape(p.cols, sizeof(T) == 4);
-  const dim3 g((unsigned)parts), b(1024);
+  const NormShape s = bwd_shape(p.cols, sizeof(T) == 4);
+  const dim3 g((unsigned)parts), b(s.tpr ? 1024 / s.tpr * s.tpr : 1024);
   switch (s.key()) {
     case 6408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 64, 8, CK, true, EXACT>), g, b, 0, st, p); break;
     case 12808: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 128, 8, CK, true, EXACT>), g, b, 0, st, p); break;
+    case 19208: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 192, 8, CK, true, EXACT>), g, b, 0, st, p); break;
     case 25608: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 256, 8, CK, true, EXACT>), g, b, 0, st, p); break;
+    case 32008: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 320, 8, CK, true, EXACT>), g, b, 0, st, p); break;
+    case 38408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 384, 8, CK, true, EXACT>), g, b, 0, st, p); break;
     case 51208: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 512, 8, CK, true, EXACT>), g, b, 0, st, p); break;
     case 102408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 1024, 8, CK, true, EXACT>), g, b, 0, st, p); break;
     default: {
@@ -598,7 +630,7 @@ hipError_t launch_bwd_any(const NormParams& p, int parts, hipStream_t st) {
 
 // Blocks of the backward, which is also the number of partial rows.
 int mxf_norm_parts(int64_t rows, int64_t cols) {
-  const NormShape s = norm_shape(cols, false);
+  const NormShape s = bwd_shape(cols, false);
   const bool one = s.ne == 8;  // dx and the column sums in one kernel
   const int64_t need = one ? (rows + 1024 / s.tpr - 1) / (1024 / s.tpr) : rows;
   const int64_t most = one ? 256 : 128;

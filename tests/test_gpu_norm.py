@@ -118,6 +118,14 @@ def test_checkpoint(rows, cols, kind):
     check_grads(mx.layer_norm_ckpt_bwd(dy, q, s, rstd, w), f64(dy), xh, f64(rstd), f64(w), rows, cols, T * np.abs(xh))
 
 
+@pytest.mark.parametrize("rows,cols", [(70, 1030), (1400, 1411), (7, 1536), (41, 2049), (600, 2304), (9, 2560), (13, 2561),
+                                       (520, 2816), (3, 3000)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_widths_between_powers_of_two(rows, cols, kind):
+    test_forward_and_backward(rows, cols, kind, kind)
+    test_checkpoint(rows, cols, kind)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols,pad,shift", [(5, 64, 8, 0), (5, 64, 3, 0), (4, 96, 0, 1), (6, 2048, 24, 8), (3, 33000, 5, 3)])
 def test_strides_and_offsets_give_the_same_bits(rows, cols, pad, shift, kind):
