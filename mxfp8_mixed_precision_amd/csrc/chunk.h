@@ -1,6 +1,5 @@
 // Rows in chunks of 16 bytes at any alignment (layer norm, SwiGLU): loads, stores, and the decoding of MXFP8
-// codes. The hardware takes 16-byte accesses at any address, so only the chunk in which a row ends needs its
-// elements one by one.
+// codes. The hardware takes 16-byte accesses at any address; only the chunk in which a row ends needs care.
 #pragma once
 #include "mx_device.h"
 
@@ -41,17 +40,31 @@ struct Elem<float> {
   }
 };
 
-// 16 bytes at column c of a row. EXACT (rows end on a chunk): a lane past the end loads column 0 instead, so
-// that the load needs no branch (after one the compiler cannot count the loads in flight and waits for all
-// of them), and is left out where the chunk is used. Else the elements that exist, and zeros.
-template <class T, bool EXACT>
+// How rows end: on a whole chunk; inside one; inside their first, or a kernel that has no other loads in flight.
+enum Ends { EXACT, INSIDE, TINY };
+
+// v >> bits (bits < 128, per lane) of a 128-bit value.
+__device__ __forceinline__ u32x4_t shr128(u32x4_t v, uint32_t bits) {
+  const uint32_t b = bits & 31;
+  u32x4_t r = {__builtin_amdgcn_alignbit(v[1], v[0], b), __builtin_amdgcn_alignbit(v[2], v[1], b),
+               __builtin_amdgcn_alignbit(v[3], v[2], b), v[3] >> b};
+  if (bits & 32) r = (u32x4_t){r[1], r[2], r[3], 0};
+  if (bits & 64) r = (u32x4_t){r[2], r[3], 0, 0};
+  return r;
+}
+
+// 16 bytes at column c of a row, without a branch: after one the compiler cannot count the loads in flight and
+// waits for all of them. The chunk in which a row ends is loaded from the row's end backwards and shifted where it
+// is used (chunk_of); a lane past the end loads one that exists, and is left out or zeroed there. TINY
+// goes element by element.
+template <class T, Ends E>
 __device__ __forceinline__ u32x4_t load_chunk(const T* row, int c, int cols) {
   u32x4_t v = {0, 0, 0, 0};
   const int n = cols - c;
-  if constexpr (EXACT) {
+  if constexpr (E == EXACT) {
     __builtin_memcpy(&v, row + (n > 0 ? c : 0), 16);
-  } else if (n >= Elem<T>::VEC) {
-    __builtin_memcpy(&v, row + c, 16);
+  } else if constexpr (E == INSIDE) {
+    __builtin_memcpy(&v, row + min(c, cols - Elem<T>::VEC), 16);
   } else if (n > 0) {
     uint32_t e[Elem<T>::VEC];
 #pragma unroll
@@ -63,16 +76,25 @@ __device__ __forceinline__ u32x4_t load_chunk(const T* row, int c, int cols) {
   }
   return v;
 }
+// The loaded chunk's elements that exist, then zeros; n: elements from column c to the row's end.
+template <class T, Ends E>
+__device__ __forceinline__ u32x4_t chunk_of(u32x4_t v, int n) {
+  if constexpr (E == INSIDE) {
+    constexpr int VEC = Elem<T>::VEC;
+    if (n < VEC) v = n > 0 ? shr128(v, (uint32_t)(VEC - n) * (128 / VEC)) : (u32x4_t){0, 0, 0, 0};
+  }
+  return v;
+}
 
 // (past the caches' retention: y and dx are larger than the caches when it matters. 16384 x 2048 backward from
 // the checkpoint 36 against 39 us, 8192 x 7168 forward 66 against 69; loads gain nothing from it.)
 typedef u32x4_t u32x4_any __attribute__((aligned(1)));
-template <class T, bool EXACT>
+template <class T, Ends E>
 __device__ __forceinline__ void store_chunk(T* p, const float* f, int n) {
   constexpr int VEC = Elem<T>::VEC;
-  if (EXACT ? n > 0 : n >= VEC) {
+  if (E == EXACT ? n > 0 : n >= VEC) {
     __builtin_nontemporal_store(Elem<T>::pack(f), reinterpret_cast<u32x4_any*>(p));
-  } else if (!EXACT) {
+  } else if (E != EXACT) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       if (i < n) p[i] = Elem<T>::put(f[i]);

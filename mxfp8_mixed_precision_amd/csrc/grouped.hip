@@ -10,6 +10,7 @@
 // enters the same matrix instruction unrounded.
 #include <type_traits>
 
+#include "chunk.h"
 #include "kernels.h"
 #include "mx_device.h"
 
@@ -212,16 +213,6 @@ __device__ __forceinline__ u32x4_t load16_any(const void* p) {
 __device__ __forceinline__ uint32_t bf16_of_fp8(uint32_t w, bool hi, float scale) {
   return __builtin_bit_cast(uint32_t, hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true)
                                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
-}
-
-// v >> bits (bits < 128, per lane) of a 128-bit value.
-__device__ __forceinline__ u32x4_t shr128(u32x4_t v, uint32_t bits) {
-  const uint32_t b = bits & 31;
-  u32x4_t r = {__builtin_amdgcn_alignbit(v[1], v[0], b), __builtin_amdgcn_alignbit(v[2], v[1], b),
-               __builtin_amdgcn_alignbit(v[3], v[2], b), v[3] >> b};
-  if (bits & 32) r = (u32x4_t){r[1], r[2], r[3], 0};
-  if (bits & 64) r = (u32x4_t){r[2], r[3], 0, 0};
-  return r;
 }
 
 // An operand that passes through registers: BF16 at any alignment, or (X8, contraction-slow) codes with

@@ -106,8 +106,8 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(SwigluParams p) {
   u32x4_t g = {0, 0, 0, 0}, u = g;
   if (n > 0) {
     const uint16_t* src = p.gu + row * p.ldgu;
-    g = load_chunk<uint16_t, EXACT>(src, c, F);
-    u = load_chunk<uint16_t, EXACT>(src + F, c, F);
+    g = load_chunk<uint16_t, EXACT ? Ends::EXACT : TINY>(src, c, F);
+    u = load_chunk<uint16_t, EXACT ? Ends::EXACT : TINY>(src + F, c, F);
     const u32x4_t h = {swiglu_h2(g[0], u[0]), swiglu_h2(g[1], u[1]), swiglu_h2(g[2], u[2]), swiglu_h2(g[3], u[3])};
     store_words<EXACT>(p.h + row * p.ldh + c, h, n);
   }
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluParams p) {
   const int F = (int)p.F, c = (int)ch * 8, n = F - c;
   const uint8_t* q = p.q + row * 2 * p.F + c;
   const uint8_t* s = p.s + row * 2 * p.G + (ch >> 2);
-  const u32x4_t d = load_chunk<uint16_t, EXACT>(p.dh + row * p.lddh, c, F);
+  const u32x4_t d = load_chunk<uint16_t, EXACT ? Ends::EXACT : TINY>(p.dh + row * p.lddh, c, F);
   uint32_t qg[2], qu[2];
   load_codes<EXACT>(q, qg, n);
   load_codes<EXACT>(q + F, qu, n);
