@@ -468,7 +468,7 @@ __global__ __launch_bounds__(1024 / TPR * TPR) void norm_bwd_kernel(NormParams p
 }
 
 // Rows too long for registers: dx alone (two passes over a row). Past 8192 columns dw and db no longer fit
-// beside a row, and a second kernel forms the column sums, a thread per column.
+// beside a row, and a second kernel forms the column sums.
 template <class T, bool CK>
 __device__ __forceinline__ float xhat_at(const NormParams& p, int64_t row, int64_t c, float mean, float rstd) {
   if constexpr (CK) {
@@ -503,21 +503,59 @@ __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormParams p) {
     }
   }
 }
-// Columns blockIdx.x * 256 + thread over rows y, y + parts, ...: partial row y. Runs before
-// norm_bwd_long_kernel, which may write dx over dy.
-template <class T, bool CK>
+// A thread's 16 bytes of columns over rows y, y + parts, ..., four rows' loads in flight: partial row y. Runs
+// before dx is written, which may be over dy. (4096 BF16 rows of 14336 from a checkpoint, the whole backward: 88 us;
+// 132 with a column per thread.)
+template <class T, bool CK, Ends E>
 __global__ __launch_bounds__(256) void norm_bwd_cols_kernel(NormParams p) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.cols) return;
-  float dw = 0.0f, db = 0.0f;
-  for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
-    const float d = Elem<T>::get(reinterpret_cast<const T*>(p.dy)[row * p.ldy + c]);
-    dw += d * xhat_at<T, CK>(p, row, c, CK ? 0.0f : p.mean[row], p.rstd[row]);
-    db += d;
+  constexpr int VEC = Elem<T>::VEC, U = 4;
+  const int cols = (int)p.cols, c = (int)(blockIdx.x * 256 + threadIdx.x) * VEC, n = cols - c;
+  if (n <= 0) return;
+  const int64_t G = (p.cols + 31) >> 5, step = gridDim.y;
+  float dw[VEC], db[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) dw[i] = db[i] = 0.0f;
+  for (int64_t row = blockIdx.y; row < p.rows; row += U * step) {
+    u32x4_t dy[U], x[U];
+    uint32_t k[U][VEC / 4], s[U];
+    float mean[U], rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = min(row + u * step, p.rows - 1);  // (past the last row: the last, not added)
+      dy[u] = load_chunk<T, E>(reinterpret_cast<const T*>(p.dy) + r * p.ldy, c, cols);
+      if constexpr (CK) {
+        __builtin_memcpy(k[u], p.q + r * p.cols + (E == INSIDE ? min(c, cols - VEC) : c), VEC);
+        s[u] = p.s[r * G + (c >> 5)];
+      } else {
+        x[u] = load_chunk<T, E>(reinterpret_cast<const T*>(p.x) + r * p.ldx, c, cols);
+        mean[u] = p.mean[r];
+        rstd[u] = p.rstd[r];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (row + u * step >= p.rows) break;
+      float d[VEC], xf[VEC];
+      Elem<T>::unpack(chunk_of<T, E>(dy[u], n), d);
+      if constexpr (CK) {
+        if (E == INSIDE) codes_of<VEC>(k[u], n);
+      } else {
+        Elem<T>::unpack(chunk_of<T, E>(x[u], n), xf);
+      }
+      const float sc = CK ? ckpt_scale(s[u]) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        dw[i] += d[i] * (CK ? ckpt_value(k[u], i, sc) : (xf[i] - mean[u]) * rstd[u]);
+        db[i] += d[i];
+      }
+    }
   }
-  float* pw = p.part + (int64_t)blockIdx.y * 2 * p.cols;
-  pw[c] = dw;
-  pw[p.cols + c] = db;
+  float* pw = p.part + (int64_t)blockIdx.y * 2 * p.cols + c;
+#pragma unroll
+  for (int i = 0; i < VEC; i += 4) {
+    store_chunk<float, INSIDE>(pw + i, dw + i, n - i);
+    store_chunk<float, INSIDE>(pw + p.cols + i, db + i, n - i);
+  }
 }
 
 // dw and db as the sum of `parts` partial rows, 32 columns a block and 32 rows at a time; the order of
@@ -614,7 +652,8 @@ hipError_t launch_bwd(const NormParams& p, int parts, hipStream_t st) {
     case 102408: hipLaunchKernelGGL((mxf::norm_bwd_kernel<T, 1024, 8, CK, true, E>), g, b, 0, st, p); break;
     default: {
       if (p.part) {
-        hipLaunchKernelGGL((mxf::norm_bwd_cols_kernel<T, CK>), dim3((unsigned)((p.cols + 255) / 256), (unsigned)parts),
+        constexpr int per = 256 * mxf::Elem<T>::VEC;
+        hipLaunchKernelGGL((mxf::norm_bwd_cols_kernel<T, CK, E>), dim3((unsigned)((p.cols + per - 1) / per), (unsigned)parts),
                            dim3(256), 0, st, p);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

@@ -126,6 +126,13 @@ def test_widths_between_powers_of_two(rows, cols, kind):
     test_checkpoint(rows, cols, kind)
 
 
+@pytest.mark.parametrize("rows,cols", [(700, 8200), (129, 9003), (260, 16392)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_many_long_rows(rows, cols, kind):
+    test_forward_and_backward(rows, cols, kind, kind)
+    test_checkpoint(rows, cols, kind)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols,pad,shift", [(5, 64, 8, 0), (5, 64, 3, 0), (4, 96, 0, 1), (6, 2048, 24, 8), (3, 33000, 5, 3)])
 def test_strides_and_offsets_give_the_same_bits(rows, cols, pad, shift, kind):
