@@ -394,11 +394,12 @@ mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, cons
  * device, may be NULL) becomes MXF_DEV_OK or MXF_DEV_BAD_OFFSETS.
  * wgrad's x: BF16 x, or (x NULL) its row-wise MXFP8, x_q [M, K] and x_s [M, ceil(K / 32)], dense, as
  * mxfp8_quantize writes them; the codes are decoded in the kernel.
- * A product too small for its tiles (few rows per expert) is bound by the weights' bytes; fwd then
- * streams each met expert's weight once.
+ * With few rows per expert the weights' bytes bound a product: fwd then streams the weight of each expert
+ * that has rows once, and wgrad writes dw at the rate of stores.
  * Limits: E in [1, 1024]; M in [0, 2^30]; N, K in [1, 2^20]; ldx >= K, ldy >= N. Pointers aligned to
- * their elements, int32 arrays to 4; rows of 16-byte alignment (N, K, ldx, ldy multiples of 8; wgrad
- * from codes: K a multiple of 32) take the fast kernels. Outputs may not overlap inputs.
+ * their elements, int32 arrays to 4; operands and outputs whose rows are 16-byte aligned (N, K, ldx, ldy
+ * multiples of 8; wgrad from codes: K a multiple of 16 and aligned codes) take the fast kernels: the others
+ * need about twice the time. Outputs may not overlap inputs.
  * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags), MXF_E_DEVICE, MXF_E_HIP. Profiling
  * names grouped_fwd, grouped_dgrad, grouped_wgrad. */
 #define MXF_GROUPED_OUT_F32 1u  /* y, dx or dw is FP32 instead of BF16 */

@@ -3,7 +3,8 @@
 The compute lives in the HIP library ``libmxfp8.so`` (C ABI: include/mxfp8.h);
 this package is its Python binding. ``MlpContext`` allocates the caller-owned
 ``saved`` and ``workspace`` buffers with torch and exposes the library's
-documented intermediate tensors as views, for tests and inspection.
+documented intermediate tensors as views, for tests and inspection. ``layer_norm_*``,
+``swiglu_ckpt_*`` and ``grouped_gemm_*`` (block_ops.py) take and return torch tensors.
 """
 from ._abi import (CAP_GFX950, COL, DEBUG_F32, DEQ_BF16, DEQ_E5M2, DEQ_F32, E5M2, DEV_BAD_EXPERT, DEV_BAD_OFFSETS, DEV_OK,
                    CONCURRENT, DEV_OVERFLOW, EXPORTS, LIB_PATH, OUT_F32, SERIAL, UNFUSED, X_QUANTIZED, dequantize,

@@ -3,8 +3,8 @@ ragged expert products (include/mxfp8.h).
 
 Each call checks its tensors, allocates its outputs with torch and makes one library call on the current
 stream of the tensors' device, or on ``stream=`` (a torch stream, or a hipStream_t as an int), which the outputs
-and the workspace then belong to; inputs that another stream made are the caller's to order. Checkpoints are row-wise MXFP8: uint8 codes and E8M0 scale
-bytes, which ``dequantize`` reads back. A violated check raises ValueError before anything is launched;
+and the workspace then belong to; inputs that another stream made are the caller's to order.
+Checkpoints are row-wise MXFP8: uint8 codes and E8M0 scale bytes, which ``dequantize`` reads back. A violated check raises ValueError before anything is launched;
 what the library itself refuses raises MxfError.
 """
 import functools

@@ -8,6 +8,11 @@
 // BF16 operands, FP32 accumulation in the matrix cores, one rounding at the store. A code of the
 // MXFP8 checkpoint has four significant bits, so its product with the scale is a BF16 number and
 // enters the same matrix instruction unrounded.
+//
+// Measured, 16 experts ragged, 24576 x 2816 x 2048: forward 262 us (1080 TFLOP/s), weight gradient 274 into BF16, 295
+// into FP32; 8 experts ragged, 16384 rows, input gradient from 7168 to 2048 columns 444 (1083), even 398; 8192^3: 781,
+// 825, 850. The main loop's bound is the matrix instructions at the clock that the power limit leaves (without any loads
+// 8192^3 forward took 732, not 826); rows without 16-byte alignment take about twice the time.
 #include <type_traits>
 
 #include "chunk.h"

@@ -6,7 +6,8 @@
 //             and h' = g' s u', which the next product's weight gradient needs and which is
 //             computed again here instead of being kept
 //
-// Bound: HBM (8.06 bytes per element of h forward, 10.06 backward with h'). h of the forward comes
+// Bound: HBM (8.06 bytes per element of h forward, 10.06 backward with h'): 24576 x 1408 takes 42 us and 53 (6.6
+// TB/s). h of the forward comes
 // from the unrounded g and u; only what is kept is rounded to 8 bits. All arithmetic is FP32 with
 // one rounding to BF16 per result.
 //
