@@ -945,10 +945,15 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
     }
   }
   // 256 x 256 tiles where they fill the chip (forward of 24576 x 2816 x 2048, 64 experts: 335 us against 390 on
-  // 128 x 128; 4096 rows, 16 experts, too few: 72 against 65); in the weight gradient twice over, since the
-  // experts' tiles differ in length (8192 rows of 4 experts, 2048 x 2048, 256 tiles: 126 against 73).
-  const bool big = op == 2 ? p.E * ((om + 255) / 256) * ((on + 255) / 256) >= 2 * ncu
-                           : (om + 255) / 256 * ((on + 255) / 256) >= ncu;
+  // 128 x 128), or where, half a tile of every expert's end counted, they take one round of the chip and the smaller
+  // ones, two to a compute unit, would take a second: forward of 8 experts, 4096 x 7168, 2816 rows 276 on 128, 186 on
+  // 256; one expert, 4096 x 4096, 2304 rows 91, 73; but 3 experts of 6000 x 2048, 1000 rows (one round of either) 32, 44;
+  // 16 experts of 2816 x 2048, 4096 rows (a second round of either) 57, 67. In the weight gradient they fill it twice
+  // over, since the experts' tiles differ in length (8192 rows of 4 experts, 2048 x 2048, 256 tiles: 73, 126).
+  const int64_t ct = (on + 255) / 256, tiles = (om + 255) / 256 * ct;
+  const bool one_round = (om + 128 * (int64_t)p.E) * ct <= 256 * ncu &&
+                         (om + 64 * (int64_t)p.E) * ((on + 127) / 128) > 128 * 2 * ncu;
+  const bool big = op == 2 ? p.E * tiles >= 2 * ncu : tiles >= ncu || one_round;
   if (op == 0)
     return aligned ? launch_tiles<0, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<0, STAGED, STAGED>(p, big, ncu, st);
   if (op == 1)

@@ -109,6 +109,21 @@ def test_large_tiles(counts, N, K, out):
     close(mx.grouped_gemm_dgrad(dy, w, toffs, out_dtype=out), dx, mdx, K, "dgrad")
 
 
+@pytest.mark.parametrize("counts,tail", [([1000, 0, 900, 300], 0), ([2304], 0), ([130, 0, 100, 7], 1963), ([0, 0, 600, 3], 1600)])
+@pytest.mark.parametrize("N,K", [(4600, 72), (4599, 71)])
+def test_less_than_a_round_of_large_tiles(counts, tail, N, K):
+    """Fewer large tiles than compute units, and a capacity of rows that is mostly not used: what is there runs
+    whole, as halves or as quarters."""
+    mx = require_gpu()
+    for n, k, op in ((N, K, mx.grouped_gemm_fwd), (K, N, mx.grouped_gemm_dgrad)):
+        offs, toffs, x, w, dy = problem(counts, n, k, n, tail)
+        (y, dx, _), (my, mdx, _) = reference(x, w, dy, offs)
+        fwd = op is mx.grouped_gemm_fwd
+        got = op(x if fwd else dy, w, toffs)
+        end = offs[-1]
+        close(got[:end], (y if fwd else dx)[:end], (my if fwd else mdx)[:end], K, "product")
+
+
 @pytest.mark.parametrize("counts,N,K", [([100, 0, 333, 64, 1, 70], 1500, 2000), ([100, 0, 333, 64, 1, 70], 1501, 1999),
                                         ([65] * 5 + [0] * 63, 400, 504)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
