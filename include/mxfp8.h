@@ -399,7 +399,7 @@ mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, cons
  * Limits: E in [1, 1024]; M in [0, 2^30]; N, K in [1, 2^20]; ldx >= K, ldy >= N. Pointers aligned to
  * their elements, int32 arrays to 4; operands and outputs whose rows are 16-byte aligned (N, K, ldx, ldy
  * multiples of 8; wgrad from codes: K a multiple of 16 and aligned codes) take the fast kernels: the others
- * need about twice the time. Outputs may not overlap inputs.
+ * need about twice the time (fwd of few rows: 4-byte alignment is enough). Outputs may not overlap inputs.
  * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags), MXF_E_DEVICE, MXF_E_HIP. Profiling
  * names grouped_fwd, grouped_dgrad, grouped_wgrad. */
 #define MXF_GROUPED_OUT_F32 1u  /* y, dx or dw is FP32 instead of BF16 */

@@ -810,6 +810,14 @@ __global__ __launch_bounds__(256, !RING ? 4 : BM == 256 ? 1 : 2) void grouped_dw
 // rows per block measured alike and 10% slower.
 constexpr int FR = 32, FN_COLS = 32, FW = 8;  // rows, columns, wavefronts of a block
 
+template <bool ANY>
+__device__ __forceinline__ u32x4_t load16(const uint16_t* p) {
+  if constexpr (ANY)
+    return load16_any(p);
+  else
+    return *reinterpret_cast<const u32x4_t*>(p);
+}
+template <bool ANY>
 __device__ __forceinline__ void few_rows(const GroupedParams& p, float* red, const uint16_t* x, const uint16_t* w, int mr,
                                          int nc) {
   constexpr int MT = FR / 16;
@@ -832,15 +840,24 @@ __device__ __forceinline__ void few_rows(const GroupedParams& p, float* red, con
     for (int u = 0; u < U; ++u) {
       const int k = (s + u) * 32 + kg;
       in[u] = s + u < s1 && k < K;
-      const int kk = in[u] ? k : 0;
+      const int kk = in[u] ? (ANY ? min(k, K - 8) : k) : 0;  // (the last eight of a row, shifted below)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fw[u][j] = *reinterpret_cast<const u32x4_t*>(wp[j] + kk);
+      for (int j = 0; j < 2; ++j) fw[u][j] = load16<ANY>(wp[j] + kk);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) fx[u][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + kk);
+      for (int i = 0; i < MT; ++i) fx[u][i] = load16<ANY>(xp[i] + kk);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const u32x4_t zero = {0, 0, 0, 0};
+      if constexpr (ANY) {
+        const int over = (s + u) * 32 + kg + 8 - K;  // elements of the lane's eight past the row's end
+        if (over > 0 && over < 8) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) fw[u][j] = shr128(fw[u][j], 16 * over);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) fx[u][i] = shr128(fx[u][i], 16 * over);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) fw[u][j] = in[u] ? fw[u][j] : zero;
 #pragma unroll
@@ -863,6 +880,7 @@ __device__ __forceinline__ void few_rows(const GroupedParams& p, float* red, con
         red[(wave * FR + i * 16 + 4 * (lane >> 4) + q) * (FN_COLS + 1) + j * 16 + r16] = acc[i][j][q];
 }
 
+template <bool ANY>
 __global__ __launch_bounds__(64 * FW, 2) void grouped_few_rows_kernel(GroupedParams p, int col_tiles) {
   __shared__ float red[FW * FR * (FN_COLS + 1)];
   const RowTiles rt = count_row_tiles(p.offs, p.E, p.M, FR);
@@ -874,7 +892,7 @@ __global__ __launch_bounds__(64 * FW, 2) void grouped_few_rows_kernel(GroupedPar
   const int mr = r.m1 - r.m0, nc = (int)min(p.N - n0, (int64_t)FN_COLS);
   const uint16_t* w = p.b + ((int64_t)r.e * p.N + n0) * p.K;
   const uint16_t* x = p.a + r.m0 * p.lda;
-  few_rows(p, red, x, w, mr, nc);
+  few_rows<ANY>(p, red, x, w, mr, nc);
   __syncthreads();
   for (int i = threadIdx.x; i < mr * FN_COLS; i += 64 * FW) {
     const int m = i / FN_COLS, n = i % FN_COLS;
@@ -937,10 +955,15 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
                        p.ldc % (p.out_f32 ? 4 : 8) == 0 && a16(p.a) && a16(p.b) && a16(p.c) && p.lda < (1 << 22) &&
                        p.ldb < (1 << 22);
   // Few rows: up to 96, or eight per expert (at 12 per expert the 128 x 128 tiles are 7% faster, at 24 16%).
-  if (op == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && a16(p.a) && a16(p.b) && (p.M <= 96 || p.M <= 8 * p.E)) {
+  // Rows that are 4-byte aligned will do (16 experts of 2816 x 2044, 48 rows: 24 us, 42 in tiles); 16-byte loads at odd
+  // elements take several times as long (2816 x 2047: 67, 53 in tiles).
+  const auto a4 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0; };
+  if (op == 0 && p.K >= 8 && p.K % 2 == 0 && p.lda % 2 == 0 && a4(p.a) && a4(p.b) && (p.M <= 96 || p.M <= 8 * p.E)) {
+    const bool any = p.K % 8 || p.lda % 8 || !a16(p.a) || !a16(p.b);
     const int64_t ct = (p.N + FN_COLS - 1) / FN_COLS, rt = p.M / FR + (p.E < p.M ? p.E : p.M);
     if (rt * ct < (1 << 22)) {  // fewer than 2^32 threads
-      hipLaunchKernelGGL(grouped_few_rows_kernel, dim3((unsigned)(rt ? rt * ct : 1)), dim3(64 * FW), 0, st, p, (int)ct);
+      hipLaunchKernelGGL(any ? grouped_few_rows_kernel<true> : grouped_few_rows_kernel<false>,
+                         dim3((unsigned)(rt ? rt * ct : 1)), dim3(64 * FW), 0, st, p, (int)ct);
       return hipGetLastError();
     }
   }

@@ -83,6 +83,12 @@ def test_products(counts, N, K, out):
     check_all(counts, N, K, sum(counts) + N + K, out)
 
 
+@pytest.mark.parametrize("counts,N,K", [([0, 3, 1, 0] * 256, 40, 48), ([0] * 1023 + [150], 40, 48), ([20, 0, 13, 30] * 256, 24, 40),
+                                        ([1] * 1024, 33, 17)])
+def test_a_thousand_experts(counts, N, K):
+    check_all(counts, N, K, 1024)
+
+
 @pytest.mark.parametrize("counts,N,K", [([700, 0, 1400, 260, 1, 2000], 1408, 768), ([1900, 333], 1000, 2056),
                                         ([40, 11, 0, 90], 2816, 2048)])
 def test_larger_products(counts, N, K):
@@ -211,6 +217,25 @@ def test_few_rows_in_one_expert_of_many(rows):
         (y, _, _), (my, _, _) = reference(x, w, dy, offs)
         for out in (torch.bfloat16, torch.float32):
             close(mx.grouped_gemm_fwd(x, w, toffs, out_dtype=out), y, my, 328, "fwd")
+
+
+@pytest.mark.parametrize("K,pad,shift", [(8, 0, 0), (10, 2, 0), (330, 0, 0), (1788, 4, 2), (334, 1, 0), (328, 0, 2), (326, 0, 1)])
+def test_few_rows_at_any_alignment(K, pad, shift):
+    """Rows of any even or odd alignment, NaN around them."""
+    mx = require_gpu()
+    offs, toffs, x, w, dy = problem([0, 3, 0, 17, 1, 9], 72, K, K)
+    (y, _, _), (my, _, _) = reference(x, w, dy, offs)
+    buf = torch.full((30 * (K + pad) + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = buf[shift:shift + 30 * (K + pad)].view(30, K + pad)[:, :K]
+    v.copy_(x)
+    wb = torch.full((w.numel() + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wv = wb[shift:shift + w.numel()].view(w.shape)
+    wv.copy_(w)
+    for out in (torch.bfloat16, torch.float32):
+        close(mx.grouped_gemm_fwd(v, wv, toffs, out_dtype=out), y, my, K, "fwd")
+    v[5] = float("inf")  # a row of its expert alone
+    bad = ~mx.grouped_gemm_fwd(v, wv, toffs).isfinite()
+    assert bool(bad[5].all()) and not bool(bad[:5].any()) and not bool(bad[6:].any())
 
 
 def test_rows_past_the_segments_are_neither_read_nor_written():
