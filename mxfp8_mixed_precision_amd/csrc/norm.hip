@@ -246,18 +246,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormPar
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * TPR + t) * VEC;
-      if (E == EXACT && c >= cols) continue;
-      float o[VEC];
+      if (E != EXACT || c < cols) {
+        float o[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        float& xh = v[j * VEC + i];
-        xh *= rstd;
-        o[i] = xh * w[j * VEC + i] + b[j * VEC + i];
+        for (int i = 0; i < VEC; ++i) {
+          float& xh = v[j * VEC + i];
+          xh *= rstd;
+          o[i] = xh * w[j * VEC + i] + b[j * VEC + i];
+        }
+        store_chunk<T, E>(y + c, o, cols - c);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j * VEC + i] = 0.0f;
       }
-      store_chunk<T, E>(y + c, o, cols - c);
-      // (EXACT: a lane that is left out counts as 0 in its group's maximum; else a lane past the end takes
-      // part with zeros, or with NaN in a row whose rstd is, as is every other of that row)
-      if (p.q) put_codes<VEC, E>(v + j * VEC, cols - c, c, p.q + row * cols, p.s + row * G);
+      // All lanes of a group take part, those past the row's end with zeros (or with NaN in a row whose rstd is, as
+      // is every other of that row): a lane that is left out also passes nothing on, and of three lanes the
+      // second would not see the third's maximum.
+      if (p.q && (E != EXACT || c < 32 * G)) put_codes<VEC, E>(v + j * VEC, cols - c, c, p.q + row * cols, p.s + row * G);
     }
     row += step;
   };

@@ -257,3 +257,21 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for a, c in zip(out, step()):
             assert torch.equal(a, c), k
+
+
+@pytest.mark.parametrize("base", [0, 480, 1376, 2976, 5120, 9984])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_last_group_of_every_length(base, kind):
+    """Checkpoints byte for byte where the last group of 32 is short: ends on whole 16-byte chunks and inside one,
+    for each number of threads that a row takes. The group's largest value visits every place in it."""
+    mx = require_gpu()
+    for rem in [r for r in range(4, 32, 4)] + [3, 13, 27, 31]:
+        rows, cols = 8 * rem, base + rem
+        x = problem(rows, cols, kind, None, base + rem)[0]
+        r = torch.arange(rows, device="cuda")
+        x[r, base + r % rem] = 12.0 * (1 + x[r, base + r % rem].abs())
+        _, rstd, q, s = mx.layer_norm_ckpt_fwd(x)
+        y, _, rstd2 = mx.layer_norm_fwd(x)
+        rq, rs = ob.mx_rows(f64(y.bfloat16()))
+        bad = [int(v) for v in ((s.cpu().numpy() != rs).any(1).sum(), (q.cpu().numpy() != rq).any(1).sum())]
+        assert bad == [0, 0] and torch.equal(rstd, rstd2), (cols, "rows with wrong scales, codes", bad)
