@@ -814,13 +814,14 @@ mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, cons
 
 // ------------------------------------------------------------------ ragged expert products
 
-static mxf_status check_grouped_desc(const mxf_grouped_desc* d, bool wgrad) {
+// has_x: ldx is the stride of a BF16 x or of dx (codes are dense).
+static mxf_status check_grouped_desc(const mxf_grouped_desc* d, bool wgrad, bool has_x) {
   if (!d) return fail(MXF_E_NULL, "desc is NULL");
   if (d->E < 1 || d->E > 1024) return fail(MXF_E_SHAPE, "E = %d: must be in [1, 1024]", d->E);
   if (d->M < 0 || d->M > ((int64_t)1 << 30)) return fail(MXF_E_SHAPE, "M = %lld: must be in [0, 2^30]", (long long)d->M);
   if (d->N < 1 || d->N > (1 << 20) || d->K < 1 || d->K > (1 << 20))
     return fail(MXF_E_SHAPE, "N = %lld, K = %lld: must be in [1, 2^20]", (long long)d->N, (long long)d->K);
-  if (d->ldx < d->K || d->ldy < d->N)
+  if ((has_x && d->ldx < d->K) || d->ldy < d->N)
     return fail(MXF_E_SHAPE, "ldx = %lld, ldy = %lld: must be at least K (%lld) and N (%lld)", (long long)d->ldx,
                 (long long)d->ldy, (long long)d->K, (long long)d->N);
   if (d->flags & ~(uint32_t)(MXF_GROUPED_OUT_F32 | MXF_GROUPED_ACCUM))
@@ -834,7 +835,7 @@ static mxf_status check_grouped_desc(const mxf_grouped_desc* d, bool wgrad) {
 static mxf_status run_grouped(int op, const char* name, const mxf_grouped_desc* d, const int32_t* offs,
                               const void* left, const void* right, const void* rq, const void* rs, void* out,
                               int32_t* status, void* stream) {
-  mxf_status s = check_grouped_desc(d, op == 2);
+  mxf_status s = check_grouped_desc(d, op == 2, op != 2 || right);
   if (s != MXF_OK) return s;
   if (!offs) return fail(MXF_E_NULL, "offs is NULL");
   if (!aligned4(offs) || !aligned4(status)) return fail(MXF_E_ALIGN, "offs or status is not 4-byte aligned");
@@ -865,7 +866,7 @@ static mxf_status run_grouped(int op, const char* name, const mxf_grouped_desc* 
   p.status = status;
   p.M = d->M; p.N = d->N; p.K = d->K; p.E = d->E;
   p.lda = op == 0 ? d->ldx : d->ldy;
-  p.ldb = op == 2 ? d->ldx : d->K;
+  p.ldb = op == 2 && right ? d->ldx : d->K;
   p.ldc = op == 0 ? d->ldy : op == 1 ? d->ldx : d->K;
   p.out_f32 = f32;
   p.accum = (d->flags & MXF_GROUPED_ACCUM) != 0;

@@ -951,7 +951,7 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
   using namespace mxf;
   const int64_t om = op == 2 ? p.N : p.M, on = op == 0 ? p.N : p.K;
   // 16-byte rows, and offsets inside a tile that a descriptor covers (256 rows of ld elements < 2 GB)
-  const bool aligned = p.N % 8 == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && (p.bq || p.ldb % 8 == 0) &&
+  const bool aligned = p.N % 8 == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && p.ldb % 8 == 0 &&
                        p.ldc % (p.out_f32 ? 4 : 8) == 0 && a16(p.a) && a16(p.b) && a16(p.c) && p.lda < (1 << 22) &&
                        p.ldb < (1 << 22);
   // Few rows: up to 96, or eight per expert (at 12 per expert the 128 x 128 tiles are 7% faster, at 24 16%).

@@ -103,6 +103,14 @@ def test_grouped_pointers_and_flags():
     assert refused(f, grouped(M=1 << 30, N=1 << 20, ldy=1 << 20), P, P, P, P) == _abi.E_SHAPE  # tiles
 
 
+def test_the_stride_of_x_is_not_used_with_codes():
+    w = mx.mxf_grouped_gemm_wgrad
+    for ldx in (95, 0, -1, 1 << 40):
+        assert refused(w, grouped(ldx=ldx), P, P, None, P, P, None) == _abi.E_NULL  # dw: past the descriptor's checks
+    assert refused(w, grouped(ldx=95), P, P, P, None, None, None) == _abi.E_SHAPE
+    assert refused(w, grouped(ldy=63), P, P, None, P, P, None) == _abi.E_SHAPE
+
+
 def test_tensor_calls_refuse_what_does_not_fit():
     bf = dict(dtype=torch.bfloat16)
     x, w, offs = torch.zeros((4, 8), **bf), torch.zeros((2, 6, 8), **bf), torch.zeros(3, dtype=torch.int32)

@@ -380,3 +380,15 @@ def test_same_bits_again_on_a_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, step())), k
+
+
+@pytest.mark.parametrize("N,K", [(96, 160), (77, 101)])
+def test_the_stride_of_x_is_not_used_with_codes(N, K):
+    mx = require_gpu()
+    offs, toffs, x, _, dy = problem([30, 0, 150], N, K, 3)
+    q, s = (torch.from_numpy(np.ascontiguousarray(t)).cuda() for t in ob.mx_rows(f64(x)))
+    want = mx.grouped_gemm_wgrad(dy, (q, s), toffs)
+    for ldx in (0, -1, 1 << 40):
+        dw = torch.full_like(want, 3.0)
+        mx.mxf_grouped_gemm_wgrad(mx.GroupedDesc(3, 0, offs[-1], N, K, ldx, N), toffs, dy, None, q, s, dw)
+        assert torch.equal(dw, want), ldx
