@@ -44,7 +44,7 @@ def _on(t, device, name):
 
 
 def _dense(t, shape, dtype, device, name):
-    if not (t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()):
+    if t is None or not (t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()):
         _bad(f"{name}: a dense {dtype} tensor of shape {shape} is needed")
     _on(t, device, name)
 
@@ -110,8 +110,8 @@ def _norm_args(x, weight, bias):
 
 def _norm_fwd(x, weight, bias, eps, stats, ckpt):
     torch = _t()
-    flags = _norm_args(x, weight, bias)
     rows, cols, ld = _rows(x, "x")
+    flags = _norm_args(x, weight, bias)
     dev = x.device
     y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
     mean = torch.empty(rows, dtype=torch.float32, device=dev) if stats and not ckpt else None
@@ -141,8 +141,8 @@ def layer_norm_ckpt_fwd(x, weight=None, bias=None, eps=1e-5):
 
 def _norm_bwd(dy, x, q, s, mean, rstd, weight):
     torch = _t()
-    flags = _norm_args(dy, weight, None)
     rows, cols, ldy = _rows(dy, "dy")
+    flags = _norm_args(dy, weight, None)
     dev = dy.device
     ldx = cols
     if x is not None:
@@ -168,6 +168,8 @@ def _norm_bwd(dy, x, q, s, mean, rstd, weight):
 @_on_stream
 def layer_norm_bwd(dy, x, mean, rstd, weight=None):
     """(dx, dweight, dbias) of layer_norm_fwd; dweight and dbias are FP32."""
+    if x is None:
+        _bad("x is needed")
     return _norm_bwd(dy, x, None, None, mean, rstd, weight)
 
 
@@ -283,18 +285,20 @@ def grouped_gemm_wgrad(dy, x, offs, out_dtype=None, accumulate=None, status=None
     if isinstance(x, (tuple, list)):
         q, s = x
         x = None
-        if not (q.dim() == 2):
+        if q is None or q.dim() != 2:
             _bad("q: a 2-D tensor is needed")
         K = ldx = q.shape[1]
         _dense(q, (M, K), torch.uint8, dy.device, "q")
         _dense(s, (M, (K + 31) // 32), torch.uint8, dy.device, "s")
     else:
-        if not (x.dtype == torch.bfloat16):
+        if x is None or x.dtype != torch.bfloat16:
             _bad("x: bfloat16 is needed")
         rows, K, ldx = _rows(x, "x")
         if not (rows == M):
             _bad(f"x has {rows} rows, dy {M}")
         _on(x, dy.device, "x")
+    if offs is None or offs.dim() != 1 or offs.numel() == 0:
+        _bad("offs: a 1-D int32 tensor [E + 1] is needed")
     E = offs.numel() - 1
     if accumulate is not None:
         if not (out_dtype in (None, torch.float32)):

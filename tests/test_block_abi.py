@@ -137,6 +137,36 @@ def test_tensor_calls_refuse_what_does_not_fit():
             fn(*args)
 
 
+def test_tensor_calls_refuse_what_is_empty_or_absent():
+    bf, u8 = dict(dtype=torch.bfloat16), dict(dtype=torch.uint8)
+    x, w, offs = torch.zeros((4, 8), **bf), torch.zeros((2, 6, 8), **bf), torch.zeros(3, dtype=torch.int32)
+    dy, f, q, s = torch.zeros((4, 6), **bf), torch.zeros(4), torch.zeros((4, 8), **u8), torch.zeros((4, 1), **u8)
+    bad = [
+        (mx.layer_norm_fwd, (x[0, 0],)), (mx.layer_norm_bwd, (x[0, 0], x, f, f)),
+        (mx.layer_norm_bwd, (x, x, None, f)), (mx.layer_norm_bwd, (x, x, f, None)), (mx.layer_norm_bwd, (x, None, f, f)),
+        (mx.layer_norm_ckpt_bwd, (x, None, s, f)), (mx.layer_norm_ckpt_bwd, (x, q, None, f)),
+        (mx.layer_norm_ckpt_bwd, (x, q, s, None)),
+        (mx.swiglu_ckpt_bwd, (x, None, s)), (mx.swiglu_ckpt_bwd, (x, torch.zeros((8, 8), **u8), None)),
+        (mx.grouped_gemm_wgrad, (dy, None, offs)), (mx.grouped_gemm_wgrad, (dy, (None, s), offs)),
+        (mx.grouped_gemm_wgrad, (dy, (q, None), offs)),
+    ]
+    for o in (None, offs[:0], offs[0], offs.view(1, 3)):
+        bad += [(mx.grouped_gemm_fwd, (x, w, o)), (mx.grouped_gemm_dgrad, (dy, w, o)), (mx.grouped_gemm_wgrad, (dy, x, o)),
+                (mx.grouped_gemm_wgrad, (dy, (q, s), o)),
+                (mx.grouped_gemm_wgrad, (dy, x, o, None, torch.zeros((2, 6, 8))))]
+    wrong = []
+    for fn, args in bad:
+        try:
+            fn(*args)
+        except ValueError:
+            continue
+        except Exception as e:  # noqa: BLE001
+            wrong.append((fn.__name__, type(e).__name__))
+            continue
+        wrong.append((fn.__name__, "accepted"))
+    assert not wrong
+
+
 @pytest.mark.parametrize("src", ["norm.hip", "swiglu_ckpt.hip", "grouped.hip"])
 def test_no_scratch_and_lds_fits(src):
     for k in _kernel_metadata(src):
