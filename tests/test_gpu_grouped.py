@@ -392,3 +392,9 @@ def test_the_stride_of_x_is_not_used_with_codes(N, K):
         dw = torch.full_like(want, 3.0)
         mx.mxf_grouped_gemm_wgrad(mx.GroupedDesc(3, 0, offs[-1], N, K, ldx, N), toffs, dy, None, q, s, dw)
         assert torch.equal(dw, want), ldx
+
+
+@pytest.mark.parametrize("E,e,rows,N,K", [(256, 200, 2000, 264, 520), (32, 20, 4000, 1032, 1024), (32, 31, 4001, 1025, 1023)])
+def test_all_rows_in_one_expert(E, e, rows, N, K):
+    """A collapsed router, where few rows per expert on average choose the kernel."""
+    check_all([0] * e + [rows] + [0] * (E - 1 - e), N, K, E)

@@ -275,3 +275,44 @@ def test_last_group_of_every_length(base, kind):
         rq, rs = ob.mx_rows(f64(y.bfloat16()))
         bad = [int(v) for v in ((s.cpu().numpy() != rs).any(1).sum(), (q.cpu().numpy() != rq).any(1).sum())]
         assert bad == [0, 0] and torch.equal(rstd, rstd2), (cols, "rows with wrong scales, codes", bad)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad,shift", [(5, 64, 3, 1), (9, 24, 8, 0), (40, 1411, 5, 3), (33, 1536, 1, 0), (33, 2560, 7, 1),
+                                                 (33, 3064, 0, 3), (33, 3071, 2, 0), (300, 8200, 3, 1), (30, 16400, 1, 5)])
+def test_strides_and_alignment_change_no_bit(rows, cols, pad, shift, kind):
+    """The columns a thread owns and the order of its sums are the width's alone."""
+    mx = require_gpu()
+    x, dy, w, b = problem(rows, cols, kind, kind, cols)
+    xs, dys = strided(x, pad, shift), strided(dy, pad, shift)
+    y, mean, rstd = mx.layer_norm_fwd(x, w, b)
+    _, _, q, s = a = mx.layer_norm_ckpt_fwd(x, w, b)
+    pairs = [((y, mean, rstd), mx.layer_norm_fwd(xs, w, b)), (a, mx.layer_norm_ckpt_fwd(xs, w, b)),
+             (mx.layer_norm_bwd(dy, x, mean, rstd, w), mx.layer_norm_bwd(dys, xs, mean, rstd, w)),
+             (mx.layer_norm_ckpt_bwd(dy, q, s, rstd, w), mx.layer_norm_ckpt_bwd(dys, q, s, rstd, w))]
+    for i, (p, r) in enumerate(pairs):
+        assert all(torch.equal(u, v) for u, v in zip(p, r)), i
+
+
+@pytest.mark.parametrize("rows,cols", [(1536000, 2816), (300000, 14400), (131100, 32800)])
+def test_offsets_past_32_bits(rows, cols):
+    """Codes past 2^32 bytes, rows of x, y, dy and dx past 2^33: the last rows are those of a call with them alone."""
+    mx = require_gpu()
+    n = 8
+    x, dy, w, b = problem(n, cols, "bf16", "bf16", 6)
+    assert (rows - n) * cols > 1 << 32
+    big = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    big[-n:] = x
+    y, rstd, q, s = mx.layer_norm_ckpt_fwd(big, w, b)
+    y1, rstd1, q1, s1 = mx.layer_norm_ckpt_fwd(x, w, b)
+    assert all(torch.equal(u[-n:], v) for u, v in ((y, y1), (rstd, rstd1), (q, q1), (s, s1)))
+    mean1 = mx.layer_norm_fwd(x, w, b)[1]
+    mean = torch.zeros(rows, device="cuda")
+    mean[-n:] = mean1
+    del y
+    g = torch.zeros_like(big)
+    g[-n:] = dy
+    assert torch.equal(mx.layer_norm_ckpt_bwd(g, q, s, rstd, w)[0][-n:], mx.layer_norm_ckpt_bwd(dy, q1, s1, rstd1, w)[0])
+    assert torch.equal(mx.layer_norm_bwd(g, big, mean, rstd, w)[0][-n:], mx.layer_norm_bwd(dy, x, mean1, rstd1, w)[0])
+    del big, g, q, s
+    torch.cuda.empty_cache()

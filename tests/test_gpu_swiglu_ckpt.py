@@ -125,3 +125,63 @@ def test_no_rows_and_gradient_against_differences():
     du = (ob.swiglu(g, u + t) - ob.swiglu(g, u - t)) / (2 * t) * d
     np.testing.assert_allclose(dgu[:, :64], dg, rtol=2.0 ** -8, atol=1e-6)
     np.testing.assert_allclose(dgu[:, 64:], du, rtol=2.0 ** -8, atol=1e-6)
+
+
+def last_rows(mx, rows, F, bwd_rows=None):
+    """The last rows of a large call are those of a call with them alone."""
+    n = 4
+    gu, dh = inputs(n, F, 17)
+    one = mx.swiglu_ckpt_fwd(gu)
+    big = torch.zeros((rows, 2 * F), dtype=torch.bfloat16, device="cuda")
+    big[-n:] = gu
+    h, q, s = mx.swiglu_ckpt_fwd(big)
+    assert torch.equal(h[-n:], one[0]) and torch.equal(q[-2 * n:], one[1]) and torch.equal(s[-2 * n:], one[2])
+    del big, h, q, s
+    torch.cuda.empty_cache()
+    rows = bwd_rows or rows
+    q = torch.zeros((2 * rows, F), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((2 * rows, -(-F // 32)), dtype=torch.uint8, device="cuda")
+    d = torch.zeros((rows, F), dtype=torch.bfloat16, device="cuda")
+    q[-2 * n:], s[-2 * n:], d[-n:] = one[1], one[2], dh
+    dgu, h = mx.swiglu_ckpt_bwd(d, q, s)
+    dgu1, h1 = mx.swiglu_ckpt_bwd(dh, one[1], one[2])
+    assert torch.equal(dgu[-n:], dgu1) and torch.equal(h[-n:], h1)
+    assert not bool(dgu[:n].any()) and not bool(h[:n].any())
+    del q, s, d, dgu, h
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("F", [7200, 7203])
+def test_offsets_past_32_bits(F):
+    mx = require_gpu()
+    last_rows(mx, (1 << 31) // F + 100, F)
+
+
+def test_more_chunks_than_a_launch_takes():
+    mx = require_gpu()
+    last_rows(mx, (1 << 29) + 1000, 1, (1 << 31) + 1000)
+
+
+def test_same_bits_again_on_a_stream_and_in_a_graph():
+    mx = require_gpu()
+    gu, dh = inputs(300, 1411, 7)
+
+    def step():
+        h, q, s = mx.swiglu_ckpt_fwd(gu)
+        return (h, q, s, *mx.swiglu_ckpt_bwd(dh, q, s))
+    first = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = mx.swiglu_ckpt_fwd(gu, stream=side)
+    other = (*other, *mx.swiglu_ckpt_bwd(dh, *other[1:], stream=side))
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in range(4):
+        gu.copy_(inputs(300, 1411, 60 + k)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, step())), k
