@@ -805,8 +805,8 @@ __global__ __launch_bounds__(256, !RING ? 4 : BM == 256 ? 1 : 2) void grouped_dw
 // in index order. Weights go from memory straight to the matrix instruction's registers (16 bytes per lane;
 // 16 columns x 32 contraction indexes are one operand of the 16 x 16 x 32 instruction), the few rows of x
 // from the L2 cache. Blocks of this size put a whole CU's loads behind every strip: one row against one
-// 4096 x 4096 expert takes 12.4 us (35 in a 128 x 128 tile), 48 rows and 16 experts of 2816 x 2048 41 us (43),
-// 64 experts and 192 rows 128 us (150; 5.6 TB/s). Non-temporal loads fetch a line's halves twice (+20%); 16 or 64
+// 4096 x 4096 expert takes 12.5 us (35 in 128 x 128 tiles), 48 rows and 16 experts of 2816 x 2048, weights from memory,
+// 40 us (45), 64 experts and 192 rows 127 us (156; 5.6 TB/s). Non-temporal loads fetch a line's halves twice (+20%); 16 or 64
 // rows per block measured alike and 10% slower.
 constexpr int FR = 32, FN_COLS = 32, FW = 8;  // rows, columns, wavefronts of a block
 
@@ -954,18 +954,28 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
   const bool aligned = p.N % 8 == 0 && p.K % 8 == 0 && p.lda % 8 == 0 && p.ldb % 8 == 0 &&
                        p.ldc % (p.out_f32 ? 4 : 8) == 0 && a16(p.a) && a16(p.b) && a16(p.c) && p.lda < (1 << 22) &&
                        p.ldb < (1 << 22);
-  // Few rows: up to 96, or eight per expert (at 12 per expert the 128 x 128 tiles are 7% faster, at 24 16%).
-  // Rows that are 4-byte aligned will do (16 experts of 2816 x 2044, 48 rows: 24 us, 42 in tiles); 16-byte loads at odd
-  // elements take several times as long (2816 x 2047: 67, 53 in tiles).
+  // Few rows: up to 96, or eight per expert, unless the weights have many strips of 128 columns. A block's own cost (the
+  // look at the offsets, 64 experts at a time, and the sum in LDS) weighs more the shorter K is, while 128 x 128
+  // tiles gain from a full chip; without 16-byte alignment they are slower, so a short K may have more strips. Us in these
+  // blocks, in tiles: one row per expert, 2816 x 2048, 16 experts 27, 33; 64 experts 88, 106; 256 experts 450, 331;
+  // four, 2048 x 1024, 16 experts 17, 19; 64 experts 58, 51; 2048 x 1408, 16 experts 26, 25; 32 experts 48, 34; 7168 x 512,
+  // 2 experts 9.1, 9.1; 8 experts 27, 16; unaligned, 2048 x 1022, 16 experts 21, 30; 64 experts 68, 66. One block per
+  // compute unit is always better: 8 rows, 1024 experts of 1024 x 1024 18, 22. The average does not see a router that
+  // sends every row to one expert: 512 rows and 64 experts of 2816 x 2048 then take 52, 20 in tiles.
+  // Rows that are 4-byte aligned will do (16 experts of 2816 x 2044, 64 rows: 45, 57); 16-byte loads at odd
+  // elements take several times as long (2816 x 2047, 48 rows: 67, 53).
   const auto a4 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0; };
-  if (op == 0 && p.K >= 8 && p.K % 2 == 0 && p.lda % 2 == 0 && a4(p.a) && a4(p.b) && (p.M <= 96 || p.M <= 8 * p.E)) {
+  const int64_t strips = (p.E < p.M ? p.E : p.M) * ((p.N + 127) / 128);
+  // strips per 1024 compute units; twice as many up to one row per expert, when many experts have none
+  const int64_t most = (p.K >= 2000 ? 7 * 1024 : aligned ? p.K : 3 * p.K) * (p.M <= p.E ? 2 : 1);
+  const bool short_grid = 4 * strips <= ncu || strips * ((p.E + 63) / 64) * 1024 <= most * ncu;
+  if (op == 0 && p.K >= 8 && p.K % 2 == 0 && p.lda % 2 == 0 && a4(p.a) && a4(p.b) && (p.M <= 96 || p.M <= 8 * p.E) &&
+      short_grid) {
     const bool any = p.K % 8 || p.lda % 8 || !a16(p.a) || !a16(p.b);
     const int64_t ct = (p.N + FN_COLS - 1) / FN_COLS, rt = p.M / FR + (p.E < p.M ? p.E : p.M);
-    if (rt * ct < (1 << 22)) {  // fewer than 2^32 threads
-      hipLaunchKernelGGL(any ? grouped_few_rows_kernel<true> : grouped_few_rows_kernel<false>,
-                         dim3((unsigned)(rt ? rt * ct : 1)), dim3(64 * FW), 0, st, p, (int)ct);
-      return hipGetLastError();
-    }
+    hipLaunchKernelGGL(any ? grouped_few_rows_kernel<true> : grouped_few_rows_kernel<false>,
+                       dim3((unsigned)(rt ? rt * ct : 1)), dim3(64 * FW), 0, st, p, (int)ct);
+    return hipGetLastError();
   }
   // 256 x 256 tiles where they fill the chip (forward of 24576 x 2816 x 2048, 64 experts: 335 us against 390 on
   // 128 x 128), or where, half a tile of every expert's end counted, they take one round of the chip and the smaller

@@ -398,3 +398,21 @@ def test_the_stride_of_x_is_not_used_with_codes(N, K):
 def test_all_rows_in_one_expert(E, e, rows, N, K):
     """A collapsed router, where few rows per expert on average choose the kernel."""
     check_all([0] * e + [rows] + [0] * (E - 1 - e), N, K, E)
+
+
+def test_few_rows_among_many_experts():
+    """The forward where every block looks for its expert past the first 64, and counts, widths and lengths on either
+    side of the choice between blocks of few rows and tiles."""
+    mx = require_gpu()
+    for E, M, N, K, out in [(1024, 8, 200, 1024, torch.bfloat16), (300, 7, 128, 40, torch.float32), (128, 32, 264, 1022, torch.bfloat16),
+                            (65, 200, 96, 2048, torch.bfloat16), (65, 200, 520, 512, torch.bfloat16),
+                            (256, 256, 264, 520, torch.float32), (256, 256, 264, 522, torch.bfloat16),
+                            (16, 64, 2048, 1024, torch.bfloat16), (32, 64, 2048, 1024, torch.bfloat16),
+                            (48, 144, 2040, 2000, torch.bfloat16), (48, 144, 2040, 1998, torch.bfloat16)]:
+        r = np.random.default_rng(E + M)
+        counts = np.bincount(np.concatenate([r.integers(0, E, M - 1), [E - 1]]), minlength=E).tolist()
+        offs, toffs, x, w, dy = problem(counts, N, K, E)
+        (y, _, _), (my, _, _) = reference(x, w, dy, offs)
+        st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+        close(mx.grouped_gemm_fwd(x, w, toffs, out_dtype=out, status=st), y, my, K, (E, M, N, K))
+        assert int(st) == mx.DEV_OK
