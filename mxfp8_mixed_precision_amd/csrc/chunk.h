@@ -40,7 +40,8 @@ struct Elem<float> {
   }
 };
 
-// How rows end: on a whole chunk; inside one; inside their first, or a kernel that has no other loads in flight.
+// How rows end: on a whole chunk; inside one; inside their first. TINY, element by element, is right for any width: SwiGLU
+// takes it wherever rows do not end on a chunk.
 enum Ends { EXACT, INSIDE, TINY };
 
 // v >> bits (bits < 128, per lane) of a 128-bit value.

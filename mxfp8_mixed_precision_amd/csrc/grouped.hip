@@ -7,12 +7,14 @@
 //
 // BF16 operands, FP32 accumulation in the matrix cores, one rounding at the store. A code of the
 // MXFP8 checkpoint has four significant bits, so its product with the scale is a BF16 number and
-// enters the same matrix instruction unrounded.
+// enters the same matrix instruction unrounded, for scales from 2^-117 on: below (groups whose largest value is under
+// 2^-109) the smallest codes leave BF16's normal range.
 //
 // Measured, 16 experts ragged, 24576 x 2816 x 2048: forward 262 us (1080 TFLOP/s), weight gradient 274 into BF16, 295
 // into FP32; 8 experts ragged, 16384 rows, input gradient from 7168 to 2048 columns 444 (1083), even 398; 8192^3: 781,
-// 825, 850. The main loop's bound is the matrix instructions at the clock that the power limit leaves (without any loads
-// 8192^3 forward took 732, not 826); rows without 16-byte alignment take about twice the time.
+// 825, 850. The matrix cores are busy 57% of the first (53% input gradient, 47% weight gradient): a tile has a compute
+// unit to itself, so nothing multiplies during its first loads and its stores, and a long main loop (8192^3: 71-75%) waits
+// for operands a tenth of its time (732 us without any loads). Rows without 16-byte alignment take about twice the time.
 #include <type_traits>
 
 #include "chunk.h"
@@ -322,7 +324,9 @@ struct StagedOperand : Operand<KC, R> {
 
 // Codes whose rows are multiples of 16 bytes: the same through bounded buffer loads (codes past the stage's
 // rows or the tile's columns read as zero), with so few instructions that a piece fits between matrix
-// instructions: piece by piece, decoded in quarter 0 and fetched in quarter 3. Weight gradient of 16 experts,
+// instructions: piece by piece, all in quarter 0: a piece of the next stage is decoded and the same piece of the stage after it fetched
+// into its registers. These fetches come before A's loads of quarter 1, so the stage's wait for all but those loads
+// covers them too. Weight gradient of 16 experts,
 // 24576 x 2816 x 2048: 298 us against 370 with the general fetch between the quarters (274 from BF16).
 template <int R>
 struct CodesOperand : Operand<false, R> {
@@ -991,7 +995,8 @@ hipError_t mxf_launch_grouped(int op, const mxf::GroupedParams& p, int ncu, hipS
     return aligned ? launch_tiles<0, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<0, STAGED, STAGED>(p, big, ncu, st);
   if (op == 1)
     return aligned ? launch_tiles<1, DIRECT, DIRECT>(p, big, ncu, st) : launch_tiles<1, STAGED, STAGED>(p, big, ncu, st);
-  // Weight gradient without the ring where experts average few rows and tiles abound (us with it, without). 64
+  // Weight gradient without the ring where experts average few rows and tiles abound (us with it, without), also
+  // where one of them has all the rows (64 experts of 1408 x 2048, 24576 rows: 477, 392). 64
   // experts of 1408 x 2048: 6144 rows 164, 120 (from codes 168, 111), 24576 rows 244, 215; 256 experts, 8192 rows
   // 397, 255 (5.8 TB/s of output); 16 experts of 2816 x 2048: 128 rows each 71, 51, 512 124, 110, 768 156, 158.
   // 1024 tiles are too few: 4 experts of 2048 x 2048, 512 rows 13.6, 15.1. Staged operands need too many registers
