@@ -395,7 +395,8 @@ mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, cons
  * wgrad's x: BF16 x, or (x NULL) its row-wise MXFP8, x_q [M, K] and x_s [M, ceil(K / 32)], dense, as
  * mxfp8_quantize writes them; the codes are decoded in the kernel.
  * With few rows per expert the weights' bytes bound a product: fwd then streams the weight of each expert
- * that has rows once, and wgrad writes dw at the rate of stores.
+ * that has rows once (more than 32 rows of one read it again from the cache), and wgrad writes dw at the rate of
+ * stores.
  * Limits: E in [1, 1024]; M in [0, 2^30]; N, K in [1, 2^20]; ldx >= K, ldy >= N. Pointers aligned to
  * their elements, int32 arrays to 4; operands and outputs whose rows are 16-byte aligned (N, K, ldx, ldy
  * multiples of 8; wgrad from codes: K a multiple of 16 and aligned codes) take the fast kernels: the others

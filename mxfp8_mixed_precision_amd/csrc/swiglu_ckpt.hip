@@ -13,8 +13,8 @@
 //
 // A thread owns eight consecutive columns of one row, of g and of u, and a 32-group is four neighbouring
 // lanes, so its maximum takes two lane exchanges. EXACT: F is a multiple of 8, so that no chunk is short: 16-byte loads
-// and stores at any alignment. Other widths are loaded element by element and take half as long again or more (8192 x
-// 1411: 27.7 us forward, 26.2 backward; 8192 x 1408: 15.3, 18.5).
+// and stores at any alignment. Other widths are loaded element by element and take 1.8 times as long forward, 1.4
+// times backward (8192 x 1411: 27.7 us, 26.2; 8192 x 1408: 15.3, 18.5).
 #include "chunk.h"
 #include "kernels.h"
 #include "mx_device.h"
