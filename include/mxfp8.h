@@ -424,6 +424,120 @@ mxf_status grouped_gemm_wgrad(const mxf_grouped_desc* desc /* host */, const int
                               const void* x, const void* x_q, const void* x_s, void* dw, int32_t* status,
                               void* stream);
 
+/* ------------------------------------------------------------------ token rows to experts and back */
+
+/* The two moves around the routed experts, and their gradients, over the layout of mxf_route_plan (any pad_multiple, 1 for
+ * none; its offs, row_assign and assign_row):
+ *   mxf_dispatch_fwd   xe[r] = x[a / topk], a = row_assign[r]; zeros for a pad row (a outside [0, tokens * topk))
+ *   mxf_combine_fwd    y[t] = sum over k of weights[t, k] h[assign_row[t * topk + k]]; weights NULL: 1, which is the
+ *                      gradient of dispatch
+ *   mxf_combine_bwd    dh[r] = weights[a] dy[a / topk], zeros for a pad row; dweights[t, k] = sum of dy[t] h[row]
+ * An assignment without a row (assign_row outside [0, rows)) adds nothing and has dweights 0; a token without any gets a
+ * row of zeros. Sums are FP32 in the order of k; y and dh are rounded once; dweights is FP32. Equal inputs give equal bits.
+ * xe, dh: rows at or past offs[E] are not written (nor are rows of assignments that row_assign and assign_row do not
+ * agree on: the plan's two maps are inverse to each other).
+ * x, xe, h, y, dy, dh: BF16, or FP32 with MXF_ROUTE_F32, row strides in elements; mxf_dispatch_fwd moves
+ * elements of `element` bytes (1, 2, 4 or 8) and takes no flag. weights [tokens, topk] BF16, or FP32 with
+ * MXF_ROUTE_WEIGHT_F32, dense.
+ * Limits: tokens * topk <= 2^30, 1 <= topk <= 64, 0 <= rows <= 2^30, 1 <= D <= 2^20, 1 <= E <= 1024, strides >= D.
+ * Pointers aligned to their elements, int32 arrays to 4; any width and alignment goes at the same rate. Without tokens the
+ * token side, without rows the row side may be NULL. Outputs may not overlap inputs.
+ * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags, element), MXF_E_DEVICE, MXF_E_HIP. Profiling names
+ * dispatch, combine_fwd, combine_bwd. */
+#define MXF_ROUTE_F32 1u         /* x, h, y, dy, dh are FP32 instead of BF16 */
+#define MXF_ROUTE_WEIGHT_F32 2u  /* weights are FP32 instead of BF16 */
+
+typedef struct {
+  int64_t tokens;
+  int64_t rows;      /* rows of xe, h and dh: the plan's m_capacity */
+  int64_t D;
+  int64_t ldx;       /* elements between token rows (x, y, dy) */
+  int64_t ldh;       /* elements between expert rows (xe, h) */
+  int64_t lddh;      /* elements between rows of dh (mxf_combine_bwd only) */
+  int32_t topk;
+  int32_t E;
+  int32_t element;   /* mxf_dispatch_fwd: bytes of an element */
+  uint32_t flags;    /* MXF_ROUTE_F32 | MXF_ROUTE_WEIGHT_F32 */
+} mxf_route_desc;
+
+mxf_status mxf_dispatch_fwd(const mxf_route_desc* desc /* host */, const int32_t* offs, const int32_t* row_assign,
+                            const int32_t* assign_row, const void* x, void* xe, void* stream);
+mxf_status mxf_combine_fwd(const mxf_route_desc* desc /* host */, const int32_t* assign_row, const void* h,
+                           const void* weights, void* y, void* stream);
+mxf_status mxf_combine_bwd(const mxf_route_desc* desc /* host */, const int32_t* offs, const int32_t* row_assign,
+                           const int32_t* assign_row, const void* dy, const void* h, const void* weights, void* dh,
+                           float* dweights, void* stream);
+
+/* ------------------------------------------------------------------ MXFP4 operands */
+
+/* Microscaled 4-bit floating point: groups of 32 share a scale 2^e (an E8M0 byte e + 127), e = clamp(floor(log2(amax)) - 2,
+ * -127, 127); elements are E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives; the sign of a zero is kept), the number
+ * nearest to v / 2^e, ties to the even code, saturated to 6 (the OCP MX v1.0 MXFP4 rule). A group with amax 0 has byte
+ * 0x00; one that holds a NaN or an infinity has 0xFF, which reads back as NaN. MXF_OPERAND_E4M3: E4M3 elements by
+ * mxfp8_quantize's rule, in the same layout.
+ *
+ * Operand of a matrix [rows, K] whose products run along K, with P = ceil(K / 128):
+ *   codes   [P][rows][64] bytes: byte j of (p, r) holds k = 128 p + 2 j in its lower four bits and the next k in its upper ones;
+ *           E4M3: [2 P][rows][64], byte j of (p, r) holds k = 64 p + j
+ *   scales  [P][rows][4] bytes: byte g of (p, r) is the scale of k in [128 p + 32 g, 128 p + 32 g + 32)
+ * K is padded to a multiple of 128 with codes and scale bytes 0. `batch` matrices follow each other.
+ *
+ * mxfp4_quantize: x [batch][rows, cols] BF16, or FP32 with MXF_OPERAND_F32 (row stride ldx, batch stride rows * ldx), each
+ * matrix along its rows (q, s: operand of [rows, cols], K = cols) and / or its columns (qt, st: operand of the transposed
+ * matrix [cols, rows], K = rows); the pair that is not wanted is NULL.
+ * Gathered (row_assign not NULL; batch 1): row r is token row_assign[r] / topk of x [tokens, cols], or zeros for a pad row, as
+ * mxf_dispatch_fwd would lay them out (offs [E + 1], row_assign [rows] of mxf_route_plan). Rows at or past offs[E] are
+ * then not written along rows, and count as zeros in the last plane along columns that holds a row (later planes are not
+ * written).
+ * mxfp4_dequantize: out [batch][rows, cols] dense, BF16 or FP32 (MXF_OPERAND_F32), of an operand along its rows: element times
+ * scale, rounded once. (The operand of a transposed matrix reads back transposed.)
+ * Limits: 0 <= batch, rows <= 2^30, 1 <= cols <= 2^20, fewer than 2^24 tiles of 128 x 128; cols <= ldx <= 2^32. x, out aligned to their elements; codes 16 bytes, scales 4. Nothing to do without batch or rows.
+ * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags), MXF_E_DEVICE, MXF_E_HIP. Profiling names
+ * mxfp4_quantize, mxfp4_dequantize. */
+#define MXF_OPERAND_F32 1u   /* the matrix is FP32 instead of BF16 */
+#define MXF_OPERAND_E4M3 2u  /* E4M3 elements instead of E2M1 */
+
+typedef struct {
+  int64_t batch;
+  int64_t rows;
+  int64_t cols;
+  int64_t ldx;      /* elements between rows of x (mxfp4_quantize) */
+  int64_t tokens;   /* gathered: rows of x; tokens * topk <= 2^30 */
+  int32_t topk;     /* gathered */
+  int32_t E;        /* gathered: offs has E + 1 entries */
+  uint32_t flags;   /* MXF_OPERAND_F32 | MXF_OPERAND_E4M3 */
+} mxf_operand_desc;
+
+mxf_status mxfp4_quantize(const mxf_operand_desc* desc /* host */, const void* x, const int32_t* offs,
+                          const int32_t* row_assign, void* q, void* s, void* qt, void* st, void* stream);
+mxf_status mxfp4_dequantize(const mxf_operand_desc* desc /* host */, const void* q, const void* s, void* out, void* stream);
+
+/* ------------------------------------------------------------------ expert products on MXFP4 operands */
+
+/* The ragged expert products on operands, FP32 accumulation in the matrix cores:
+ *   grouped_gemm_mxfp4_fwd    y[r, n] = sum over k of x[r, k] w[e, n, k]: x the operand of [M, K], w of E matrices [N, K], rows
+ *                             [offs[e], offs[e+1]) of x belong to expert e, any count. With dy for x and w's operands along
+ *                             columns this is the input gradient.
+ *   grouped_gemm_mxfp4_wgrad  dw[e, n, k] = sum over e's rows r of dy[r, n] x[r, k], from the operands of dy and x along
+ *                             columns: dy of [N, M], x of [K, M]; offs multiples of 128 (mxf_route_plan with
+ *                             pad_multiple 128 or 256; pad rows are zero codes). dw dense; an expert without rows gets zeros.
+ * w, and wgrad's x, are E2M1; x, and wgrad's dy, E2M1, or E4M3 with MXF_GROUPED_LEFT_E4M3. E2M1 products are exact to FP32's
+ * last bits (3e-7 of the sum of magnitudes); with E4M3 the matrix cores add with fewer bits (4e-5).
+ * A group with scale byte 0xFF makes NaN of the outputs that it enters.
+ * desc: as grouped_gemm_*, flags MXF_GROUPED_OUT_F32 | MXF_GROUPED_ACCUM (wgrad) | MXF_GROUPED_LEFT_E4M3; ldy is y's row stride
+ * (forward); ldx is not used. Codes 16-byte aligned, scales 4; y and dw aligned to their elements. offs on the device, its
+ * contract and *status as for grouped_gemm_*; rows at or past offs[E] are never written.
+ * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags), MXF_E_DEVICE, MXF_E_HIP. Profiling
+ * names mxfp4_fwd, mxfp4_wgrad. */
+#define MXF_GROUPED_LEFT_E4M3 4u
+
+mxf_status grouped_gemm_mxfp4_fwd(const mxf_grouped_desc* desc /* host */, const int32_t* offs, const void* x_q,
+                                  const void* x_s, const void* w_q, const void* w_s, void* y, int32_t* status,
+                                  void* stream);
+mxf_status grouped_gemm_mxfp4_wgrad(const mxf_grouped_desc* desc /* host */, const int32_t* offs, const void* dy_q,
+                                    const void* dy_s, const void* x_q, const void* x_s, void* dw, int32_t* status,
+                                    void* stream);
+
 /* Synchronises `stream` and copies the device status word of the last fwd/bwd call that
  * used `workspace` into *device_status (MXF_DEV_OK or MXF_DEV_BAD_OFFSETS). */
 mxf_status mxf_read_status(const void* workspace, void* stream, int32_t* device_status /* host */);
@@ -441,7 +555,8 @@ mxf_status mxf_read_status(const void* workspace, void* stream, int32_t* device_
  * tiles: pad_multiple 256, D and 2F multiples of 256, not with MXF_CONCURRENT; otherwise
  * fc2_wgrad, fc1_wgrad, fc1_dgrad) (MXF_UNFUSED: fc1, swiglu_quant, fc2_dgrad, dswiglu_quant),
  * quantize, dequantize, route_plan, permute, dispatch_quant_x, norm_fwd, norm_bwd, swiglu_ckpt_fwd,
- * swiglu_ckpt_bwd, grouped_fwd, grouped_dgrad, grouped_wgrad, hbm_read, hbm_write, hbm_copy.
+ * swiglu_ckpt_bwd, grouped_fwd, grouped_dgrad, grouped_wgrad, dispatch, combine_fwd, combine_bwd, mxfp4_quantize,
+ * mxfp4_dequantize, mxfp4_fwd, mxfp4_wgrad, hbm_read, hbm_write, hbm_copy.
  * Errors: MXF_E_ARG (capacity < 1 or > 1<<20, or end without begin), MXF_E_NULL, MXF_E_HIP. */
 typedef struct {
   char name[32];

@@ -4,7 +4,8 @@ The compute lives in the HIP library ``libmxfp8.so`` (C ABI: include/mxfp8.h);
 this package is its Python binding. ``MlpContext`` allocates the caller-owned
 ``saved`` and ``workspace`` buffers with torch and exposes the library's
 documented intermediate tensors as views, for tests and inspection. ``layer_norm_*``,
-``swiglu_ckpt_*`` and ``grouped_gemm_*`` (block_ops.py) take and return torch tensors.
+``swiglu_ckpt_*`` and ``grouped_gemm_*`` (block_ops.py), ``dispatch_*``, ``combine_*`` and
+``mxfp4_*`` / ``grouped_gemm_mxfp4_*`` (expert_ops.py) take and return torch tensors.
 """
 from ._abi import (CAP_GFX950, COL, DEBUG_F32, DEQ_BF16, DEQ_E5M2, DEQ_F32, E5M2, DEV_BAD_EXPERT, DEV_BAD_OFFSETS, DEV_OK,
                    CONCURRENT, DEV_OVERFLOW, EXPORTS, LIB_PATH, OUT_F32, SERIAL, UNFUSED, X_QUANTIZED, dequantize,
@@ -16,10 +17,14 @@ from ._abi import (CAP_GFX950, COL, DEBUG_F32, DEQ_BF16, DEQ_E5M2, DEQ_F32, E5M2
                    mfma_probe, MFMA_MATRIX, MFMA_STAGE, NormDesc, GroupedDesc, NORM_F32, NORM_WEIGHT_F32,
                    GROUPED_OUT_F32, GROUPED_ACCUM, layer_norm_workspace_bytes, mxf_layer_norm_fwd,
                    mxf_layer_norm_bwd, mxf_swiglu_ckpt_fwd, mxf_swiglu_ckpt_bwd, mxf_grouped_gemm_fwd,
-                   mxf_grouped_gemm_dgrad, mxf_grouped_gemm_wgrad)
+                   mxf_grouped_gemm_dgrad, mxf_grouped_gemm_wgrad, RouteDesc, OperandDesc, ROUTE_F32, ROUTE_WEIGHT_F32,
+                   OPERAND_F32, OPERAND_E4M3, GROUPED_LEFT_E4M3, mxf_dispatch_fwd, mxf_combine_fwd, mxf_combine_bwd,
+                   mxf_mxfp4_quantize, mxf_mxfp4_dequantize, mxf_grouped_gemm_mxfp4_fwd, mxf_grouped_gemm_mxfp4_wgrad)
 from .block_ops import (grouped_gemm_dgrad, grouped_gemm_fwd, grouped_gemm_wgrad, layer_norm_bwd,
                         layer_norm_ckpt_bwd, layer_norm_ckpt_fwd, layer_norm_fwd, swiglu_ckpt_bwd,
                         swiglu_ckpt_fwd)
+from .expert_ops import (combine_bwd, combine_fwd, dispatch_bwd, dispatch_fwd, grouped_gemm_mxfp4_fwd,
+                         grouped_gemm_mxfp4_wgrad, mxfp4_dequantize, mxfp4_quantize)
 
 # shapes of the documented tensors, as functions of (E, D, F, m_capacity)
 _SHAPES = {

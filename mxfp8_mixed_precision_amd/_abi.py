@@ -24,7 +24,9 @@ ROW, COL, E5M2 = 1, 2, 4
 OUT_F32, DEBUG_F32, SERIAL, UNFUSED, X_QUANTIZED, CONCURRENT = 1, 2, 4, 8, 16, 32
 DEQ_BF16, DEQ_F32, DEQ_E5M2 = 0, 1, 2
 NORM_F32, NORM_WEIGHT_F32 = 1, 2
-GROUPED_OUT_F32, GROUPED_ACCUM = 1, 2
+GROUPED_OUT_F32, GROUPED_ACCUM, GROUPED_LEFT_E4M3 = 1, 2, 4
+ROUTE_F32, ROUTE_WEIGHT_F32 = 1, 2
+OPERAND_F32, OPERAND_E4M3 = 1, 2
 
 # tensor ids (mxf_tensor)
 TENSORS = ["STATUS", "XQ_R", "XS_R", "XQ_C", "XS_C", "W13Q_R", "W13S_R", "W13Q_C", "W13S_C",
@@ -41,7 +43,9 @@ EXPORTS = ["mxf_abi_version", "mxf_query_device", "mxf_last_error", "mxfp8_quant
            "mxfp8_dispatch_quantize", "mxf_hbm_probe", "mxf_mfma_probe",
            "mxf_layer_norm_fwd", "mxf_layer_norm_bwd", "mxf_layer_norm_workspace_bytes",
            "mxf_swiglu_ckpt_fwd", "mxf_swiglu_ckpt_bwd",
-           "grouped_gemm_fwd", "grouped_gemm_dgrad", "grouped_gemm_wgrad"]
+           "grouped_gemm_fwd", "grouped_gemm_dgrad", "grouped_gemm_wgrad",
+           "mxf_dispatch_fwd", "mxf_combine_fwd", "mxf_combine_bwd", "mxfp4_quantize", "mxfp4_dequantize",
+           "grouped_gemm_mxfp4_fwd", "grouped_gemm_mxfp4_wgrad"]
 
 
 class MxfError(RuntimeError):
@@ -69,6 +73,17 @@ class NormDesc(ctypes.Structure):
 class GroupedDesc(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("flags", ctypes.c_uint32), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ldh", ctypes.c_int64), ("lddh", ctypes.c_int64), ("topk", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("element", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class OperandDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("topk", ctypes.c_int32), ("E", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 _lib = None
@@ -117,6 +132,13 @@ def lib():
             "grouped_gemm_fwd": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp]),
             "grouped_gemm_dgrad": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp]),
             "grouped_gemm_wgrad": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp, vp, vp]),
+            "mxf_dispatch_fwd": (ctypes.c_int, [ctypes.POINTER(RouteDesc), vp, vp, vp, vp, vp, vp]),
+            "mxf_combine_fwd": (ctypes.c_int, [ctypes.POINTER(RouteDesc), vp, vp, vp, vp, vp]),
+            "mxf_combine_bwd": (ctypes.c_int, [ctypes.POINTER(RouteDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "mxfp4_quantize": (ctypes.c_int, [ctypes.POINTER(OperandDesc), vp, vp, vp, vp, vp, vp, vp, vp]),
+            "mxfp4_dequantize": (ctypes.c_int, [ctypes.POINTER(OperandDesc), vp, vp, vp, vp]),
+            "grouped_gemm_mxfp4_fwd": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp, vp, vp]),
+            "grouped_gemm_mxfp4_wgrad": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -375,6 +397,47 @@ def mxf_grouped_gemm_wgrad(desc, offs, dy, x, x_q, x_s, dw, status=None, stream=
     """Raw call of grouped_gemm_wgrad."""
     _check(lib().grouped_gemm_wgrad(ctypes.byref(desc), _ptr(offs), _ptr(dy), _ptr(x), _ptr(x_q), _ptr(x_s),
                                     _ptr(dw), _ptr(status), _stream(stream)))
+
+
+def mxf_dispatch_fwd(desc, offs, row_assign, assign_row, x, xe, stream=None):
+    """Raw call: pointers (tensors or ints) and a RouteDesc, as in the C header."""
+    _check(lib().mxf_dispatch_fwd(ctypes.byref(desc), _ptr(offs), _ptr(row_assign), _ptr(assign_row), _ptr(x), _ptr(xe),
+                                  _stream(stream)))
+
+
+def mxf_combine_fwd(desc, assign_row, h, weights, y, stream=None):
+    """Raw call: pointers (tensors or ints) and a RouteDesc, as in the C header."""
+    _check(lib().mxf_combine_fwd(ctypes.byref(desc), _ptr(assign_row), _ptr(h), _ptr(weights), _ptr(y),
+                                 _stream(stream)))
+
+
+def mxf_combine_bwd(desc, offs, row_assign, assign_row, dy, h, weights, dh, dweights, stream=None):
+    """Raw call: pointers (tensors or ints) and a RouteDesc, as in the C header."""
+    _check(lib().mxf_combine_bwd(ctypes.byref(desc), _ptr(offs), _ptr(row_assign), _ptr(assign_row), _ptr(dy), _ptr(h),
+                                 _ptr(weights), _ptr(dh), _ptr(dweights), _stream(stream)))
+
+
+def mxf_mxfp4_quantize(desc, x, offs, row_assign, q, s, qt, st, stream=None):
+    """Raw call of mxfp4_quantize: pointers (tensors or ints) and an OperandDesc, as in the C header."""
+    _check(lib().mxfp4_quantize(ctypes.byref(desc), _ptr(x), _ptr(offs), _ptr(row_assign), _ptr(q), _ptr(s), _ptr(qt),
+                                _ptr(st), _stream(stream)))
+
+
+def mxf_mxfp4_dequantize(desc, q, s, out, stream=None):
+    """Raw call of mxfp4_dequantize."""
+    _check(lib().mxfp4_dequantize(ctypes.byref(desc), _ptr(q), _ptr(s), _ptr(out), _stream(stream)))
+
+
+def mxf_grouped_gemm_mxfp4_fwd(desc, offs, x_q, x_s, w_q, w_s, y, status=None, stream=None):
+    """Raw call of grouped_gemm_mxfp4_fwd: pointers (tensors or ints) and a GroupedDesc, as in the C header."""
+    _check(lib().grouped_gemm_mxfp4_fwd(ctypes.byref(desc), _ptr(offs), _ptr(x_q), _ptr(x_s), _ptr(w_q), _ptr(w_s),
+                                        _ptr(y), _ptr(status), _stream(stream)))
+
+
+def mxf_grouped_gemm_mxfp4_wgrad(desc, offs, dy_q, dy_s, x_q, x_s, dw, status=None, stream=None):
+    """Raw call of grouped_gemm_mxfp4_wgrad."""
+    _check(lib().grouped_gemm_mxfp4_wgrad(ctypes.byref(desc), _ptr(offs), _ptr(dy_q), _ptr(dy_s), _ptr(x_q), _ptr(x_s),
+                                          _ptr(dw), _ptr(status), _stream(stream)))
 
 
 def profile_begin(capacity=4096):

@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp8.so")
 SOURCES = ["abi.hip", "quantize.hip", "gemm.hip", "dispatch.hip", "hbm.hip", "mfma_probe.hip",
-           "norm.hip", "swiglu_ckpt.hip", "grouped.hip"]
+           "norm.hip", "swiglu_ckpt.hip", "grouped.hip", "combine.hip", "mxfp4.hip", "grouped_mx.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -814,13 +814,19 @@ mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, cons
 
 // ------------------------------------------------------------------ ragged expert products
 
-// has_x: ldx is the stride of a BF16 x or of dx (codes are dense).
-static mxf_status check_grouped_desc(const mxf_grouped_desc* d, bool wgrad, bool has_x) {
+static mxf_status check_grouped_sizes(const mxf_grouped_desc* d) {
   if (!d) return fail(MXF_E_NULL, "desc is NULL");
   if (d->E < 1 || d->E > 1024) return fail(MXF_E_SHAPE, "E = %d: must be in [1, 1024]", d->E);
   if (d->M < 0 || d->M > ((int64_t)1 << 30)) return fail(MXF_E_SHAPE, "M = %lld: must be in [0, 2^30]", (long long)d->M);
   if (d->N < 1 || d->N > (1 << 20) || d->K < 1 || d->K > (1 << 20))
     return fail(MXF_E_SHAPE, "N = %lld, K = %lld: must be in [1, 2^20]", (long long)d->N, (long long)d->K);
+  return MXF_OK;
+}
+
+// has_x: ldx is the stride of a BF16 x or of dx (codes are dense).
+static mxf_status check_grouped_desc(const mxf_grouped_desc* d, bool wgrad, bool has_x) {
+  mxf_status s = check_grouped_sizes(d);
+  if (s != MXF_OK) return s;
   if ((has_x && d->ldx < d->K) || d->ldy < d->N)
     return fail(MXF_E_SHAPE, "ldx = %lld, ldy = %lld: must be at least K (%lld) and N (%lld)", (long long)d->ldx,
                 (long long)d->ldy, (long long)d->K, (long long)d->N);
@@ -891,6 +897,254 @@ mxf_status grouped_gemm_wgrad(const mxf_grouped_desc* desc, const int32_t* offs,
                               const void* x_q, const void* x_s, void* dw, int32_t* status, void* stream) {
   g_err.clear();
   return run_grouped(2, "grouped_wgrad", desc, offs, dy, x, x_q, x_s, dw, status, stream);
+}
+
+// ------------------------------------------------------------------ token rows to experts and back
+
+// Blocks of a launch: a kernel's grid holds fewer than 2^24 blocks of 256 threads.
+constexpr int64_t kMostBlocks = 0xFFFFFF;
+
+static mxf_status check_route_desc(const mxf_route_desc* d, uint32_t flags) {
+  if (!d) return fail(MXF_E_NULL, "desc is NULL");
+  mxf_status st = check_plan_sizes(d->tokens, d->topk, d->E);
+  if (st != MXF_OK) return st;
+  if (d->rows < 0 || d->rows > ((int64_t)1 << 30))
+    return fail(MXF_E_SHAPE, "rows = %lld: must be in [0, 2^30]", (long long)d->rows);
+  if (d->D < 1 || d->D > (1 << 20)) return fail(MXF_E_SHAPE, "D = %lld: must be in [1, 2^20]", (long long)d->D);
+  if (d->ldx < d->D || d->ldh < d->D)
+    return fail(MXF_E_SHAPE, "ldx = %lld, ldh = %lld: must be at least D (%lld)", (long long)d->ldx, (long long)d->ldh,
+                (long long)d->D);
+  if (d->flags & ~flags) return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
+  if ((d->tokens * ((d->D + 255) / 256) + d->rows / 16) / 4 + 2 > kMostBlocks)
+    return fail(MXF_E_SHAPE, "tokens = %lld, rows = %lld, D = %lld: too many blocks", (long long)d->tokens,
+                (long long)d->rows, (long long)d->D);
+  return MXF_OK;
+}
+
+static mxf::RouteParams route_params(const mxf_route_desc* d) {
+  mxf::RouteParams p = {};
+  p.E = d->E; p.topk = d->topk;
+  p.tokens = d->tokens; p.rows = d->rows; p.D = d->D;
+  p.ldx = d->ldx; p.ldh = d->ldh; p.lddh = d->lddh;
+  p.w_f32 = (d->flags & MXF_ROUTE_WEIGHT_F32) != 0;
+  return p;
+}
+
+// The plan's arrays, where rows are written.
+static mxf_status check_route_maps(const mxf_route_desc* d, const int32_t* offs, const int32_t* row_assign,
+                                   const int32_t* assign_row) {
+  if (d->rows > 0 && (!offs || !row_assign)) return fail(MXF_E_NULL, "offs or row_assign is NULL");
+  if (d->tokens > 0 && !assign_row) return fail(MXF_E_NULL, "assign_row is NULL");
+  if (!aligned4(offs) || !aligned4(row_assign) || !aligned4(assign_row))
+    return fail(MXF_E_ALIGN, "an int32 pointer is not 4-byte aligned");
+  return MXF_OK;
+}
+
+mxf_status mxf_dispatch_fwd(const mxf_route_desc* d, const int32_t* offs, const int32_t* row_assign,
+                            const int32_t* assign_row, const void* x, void* xe, void* stream) {
+  g_err.clear();
+  mxf_status st = check_route_desc(d, 0);
+  if (st != MXF_OK) return st;
+  const int32_t n = d->element;
+  if (n != 1 && n != 2 && n != 4 && n != 8) return fail(MXF_E_ARG, "element = %d bytes: must be 1, 2, 4 or 8", n);
+  if ((st = check_route_maps(d, offs, row_assign, assign_row)) != MXF_OK) return st;
+  if (d->tokens > 0 && !x) return fail(MXF_E_NULL, "x is NULL");
+  if (d->rows > 0 && !xe) return fail(MXF_E_NULL, "xe is NULL");
+  if (!aligned_to(x, n) || !aligned_to(xe, n)) return fail(MXF_E_ALIGN, "x or xe is not aligned to its elements");
+  if (d->rows == 0) return MXF_OK;
+  if ((st = check_device()) != MXF_OK) return st;
+  mxf::RouteParams p = route_params(d);
+  p.offs = offs; p.row_assign = row_assign; p.assign_row = assign_row;
+  p.D *= n; p.ldx *= n; p.ldh *= n;
+  p.x = x; p.h = xe;
+  MXF_HIP(timed("dispatch", (hipStream_t)stream, [&] { return mxf_launch_dispatch(p, (hipStream_t)stream); }),
+          "dispatch launch");
+  return MXF_OK;
+}
+
+mxf_status mxf_combine_fwd(const mxf_route_desc* d, const int32_t* assign_row, const void* h, const void* weights,
+                           void* y, void* stream) {
+  g_err.clear();
+  mxf_status st = check_route_desc(d, MXF_ROUTE_F32 | MXF_ROUTE_WEIGHT_F32);
+  if (st != MXF_OK) return st;
+  if (d->tokens == 0) return MXF_OK;
+  const bool f32 = (d->flags & MXF_ROUTE_F32) != 0;
+  const size_t n = f32 ? 4 : 2;
+  if (!assign_row || !y || (d->rows > 0 && !h)) return fail(MXF_E_NULL, "assign_row, h or y is NULL");
+  if (!aligned4(assign_row)) return fail(MXF_E_ALIGN, "assign_row is not 4-byte aligned");
+  if (!aligned_to(h, n) || !aligned_to(y, n) || !aligned_to(weights, (d->flags & MXF_ROUTE_WEIGHT_F32) ? 4 : 2))
+    return fail(MXF_E_ALIGN, "h, y or weights is not aligned to its elements");
+  if ((st = check_device()) != MXF_OK) return st;
+  mxf::RouteParams p = route_params(d);
+  p.assign_row = assign_row;
+  p.h = const_cast<void*>(h); p.w = weights; p.y = y;
+  MXF_HIP(timed("combine_fwd", (hipStream_t)stream, [&] { return mxf_launch_combine(p, f32, (hipStream_t)stream); }),
+          "combine launch");
+  return MXF_OK;
+}
+
+mxf_status mxf_combine_bwd(const mxf_route_desc* d, const int32_t* offs, const int32_t* row_assign,
+                           const int32_t* assign_row, const void* dy, const void* h, const void* weights, void* dh,
+                           float* dweights, void* stream) {
+  g_err.clear();
+  mxf_status st = check_route_desc(d, MXF_ROUTE_F32 | MXF_ROUTE_WEIGHT_F32);
+  if (st != MXF_OK) return st;
+  if (d->lddh < d->D)
+    return fail(MXF_E_SHAPE, "lddh = %lld: must be at least D (%lld)", (long long)d->lddh, (long long)d->D);
+  if ((st = check_route_maps(d, offs, row_assign, assign_row)) != MXF_OK) return st;
+  const bool f32 = (d->flags & MXF_ROUTE_F32) != 0;
+  const size_t n = f32 ? 4 : 2;
+  if (d->tokens > 0 && (!dy || !weights || !dweights)) return fail(MXF_E_NULL, "dy, weights or dweights is NULL");
+  if (d->rows > 0 && (!h || !dh)) return fail(MXF_E_NULL, "h or dh is NULL");
+  if (!aligned_to(dy, n) || !aligned_to(h, n) || !aligned_to(dh, n) || !aligned4(dweights) ||
+      !aligned_to(weights, (d->flags & MXF_ROUTE_WEIGHT_F32) ? 4 : 2))
+    return fail(MXF_E_ALIGN, "dy, h, dh, weights or dweights is not aligned to its elements");
+  if (d->tokens == 0 && d->rows == 0) return MXF_OK;
+  if ((st = check_device()) != MXF_OK) return st;
+  mxf::RouteParams p = route_params(d);
+  p.offs = offs; p.row_assign = row_assign; p.assign_row = assign_row;
+  p.dy = dy; p.h = const_cast<void*>(h); p.w = weights; p.dh = dh; p.dw = dweights;
+  MXF_HIP(timed("combine_bwd", (hipStream_t)stream, [&] { return mxf_launch_combine_bwd(p, f32, (hipStream_t)stream); }),
+          "combine gradient launch");
+  return MXF_OK;
+}
+
+// ------------------------------------------------------------------ MXFP4 operands and products
+
+static mxf_status check_operand_desc(const mxf_operand_desc* d) {
+  if (!d) return fail(MXF_E_NULL, "desc is NULL");
+  if (d->batch < 0 || d->rows < 0 || d->batch > ((int64_t)1 << 30) || d->rows > ((int64_t)1 << 30))
+    return fail(MXF_E_SHAPE, "batch = %lld, rows = %lld: must be in [0, 2^30]", (long long)d->batch, (long long)d->rows);
+  if (d->cols < 1 || d->cols > (1 << 20)) return fail(MXF_E_SHAPE, "cols = %lld: must be in [1, 2^20]", (long long)d->cols);
+  if (d->flags & ~(uint32_t)(MXF_OPERAND_F32 | MXF_OPERAND_E4M3)) return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
+  const int64_t tiles = ((d->rows + 127) / 128) * ((d->cols + 127) / 128);
+  if (d->batch > 0 && tiles > kMostBlocks / d->batch)
+    return fail(MXF_E_SHAPE, "batch = %lld, rows = %lld, cols = %lld: more than 2^24 tiles", (long long)d->batch,
+                (long long)d->rows, (long long)d->cols);
+  return MXF_OK;
+}
+
+static mxf_status check_operand_ptrs(const void* q, const void* s, const char* what) {
+  if (!aligned16(q)) return fail(MXF_E_ALIGN, "%s: the codes are not 16-byte aligned", what);
+  if (!aligned4(s)) return fail(MXF_E_ALIGN, "%s: the scales are not 4-byte aligned", what);
+  return MXF_OK;
+}
+
+static mxf::Mx4Params operand_params(const mxf_operand_desc* d) {
+  mxf::Mx4Params p = {};
+  p.batch = d->batch; p.rows = d->rows; p.cols = d->cols;
+  p.ldx = d->ldx; p.xs = d->rows * d->ldx;
+  p.tokens = d->tokens; p.topk = d->topk; p.E = d->E;
+  return p;
+}
+
+mxf_status mxfp4_quantize(const mxf_operand_desc* d, const void* x, const int32_t* offs, const int32_t* row_assign, void* q,
+                          void* s, void* qt, void* st, void* stream) {
+  g_err.clear();
+  mxf_status c = check_operand_desc(d);
+  if (c != MXF_OK) return c;
+  if (d->ldx < d->cols || d->ldx > ((int64_t)1 << 32))
+    return fail(MXF_E_SHAPE, "ldx = %lld: must be at least cols (%lld), at most 2^32", (long long)d->ldx, (long long)d->cols);
+  if (row_assign) {
+    if (d->batch != 1) return fail(MXF_E_SHAPE, "batch = %lld: must be 1 with row_assign", (long long)d->batch);
+    if ((c = check_plan_sizes(d->tokens, d->topk, d->E)) != MXF_OK) return c;
+  }
+  if (!q != !s || !qt != !st) return fail(MXF_E_NULL, "codes without scales, or scales without codes");
+  if (d->batch == 0 || d->rows == 0) return MXF_OK;
+  if (!q && !qt) return fail(MXF_E_NULL, "no output");
+  if (row_assign && !offs) return fail(MXF_E_NULL, "offs is NULL");
+  if (!x && !(row_assign && d->tokens == 0)) return fail(MXF_E_NULL, "x is NULL");
+  if (!aligned4(offs) || !aligned4(row_assign)) return fail(MXF_E_ALIGN, "offs or row_assign is not 4-byte aligned");
+  const bool f32 = (d->flags & MXF_OPERAND_F32) != 0;
+  if (!aligned_to(x, f32 ? 4 : 2)) return fail(MXF_E_ALIGN, "x is not aligned to its elements");
+  if ((c = check_operand_ptrs(q, s, "along rows")) != MXF_OK || (c = check_operand_ptrs(qt, st, "along columns")) != MXF_OK)
+    return c;
+  if ((c = check_device()) != MXF_OK) return c;
+  mxf::Mx4Params p = operand_params(d);
+  p.x = x;
+  p.q = (uint8_t*)q; p.s = (uint8_t*)s; p.qt = (uint8_t*)qt; p.st = (uint8_t*)st;
+  p.offs = offs; p.row_assign = row_assign;
+  MXF_HIP(timed("mxfp4_quantize", (hipStream_t)stream, [&] {
+            return mxf_launch_mxfp4_quantize(p, f32, (d->flags & MXF_OPERAND_E4M3) != 0, (hipStream_t)stream);
+          }), "MXFP4 quantizer launch");
+  return MXF_OK;
+}
+
+mxf_status mxfp4_dequantize(const mxf_operand_desc* d, const void* q, const void* s, void* out, void* stream) {
+  g_err.clear();
+  mxf_status c = check_operand_desc(d);
+  if (c != MXF_OK) return c;
+  if (d->batch == 0 || d->rows == 0) return MXF_OK;
+  if (!q || !s || !out) return fail(MXF_E_NULL, "q, s or out is NULL");
+  const bool f32 = (d->flags & MXF_OPERAND_F32) != 0;
+  if ((c = check_operand_ptrs(q, s, "operand")) != MXF_OK) return c;
+  if (!aligned_to(out, f32 ? 4 : 2)) return fail(MXF_E_ALIGN, "out is not aligned to its elements");
+  if ((c = check_device()) != MXF_OK) return c;
+  mxf::Mx4Params p = operand_params(d);
+  p.q = (uint8_t*)const_cast<void*>(q); p.s = (uint8_t*)const_cast<void*>(s);
+  p.out = out;
+  MXF_HIP(timed("mxfp4_dequantize", (hipStream_t)stream, [&] {
+            return mxf_launch_mxfp4_dequantize(p, f32, (d->flags & MXF_OPERAND_E4M3) != 0, (hipStream_t)stream);
+          }), "MXFP4 decoder launch");
+  return MXF_OK;
+}
+
+static mxf_status run_grouped_mx(bool wgrad, const char* name, const mxf_grouped_desc* d, const int32_t* offs,
+                                 const void* a, const void* as, const void* b, const void* bs, void* out,
+                                 int32_t* status, void* stream) {
+  mxf_status s = check_grouped_sizes(d);
+  if (s != MXF_OK) return s;
+  if (!wgrad && d->ldy < d->N)
+    return fail(MXF_E_SHAPE, "ldy = %lld: must be at least N (%lld)", (long long)d->ldy, (long long)d->N);
+  if (d->flags & ~(uint32_t)(MXF_GROUPED_OUT_F32 | MXF_GROUPED_ACCUM | MXF_GROUPED_LEFT_E4M3))
+    return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
+  if ((d->flags & MXF_GROUPED_ACCUM) && (!wgrad || !(d->flags & MXF_GROUPED_OUT_F32)))
+    return fail(MXF_E_ARG, "flags = 0x%x: MXF_GROUPED_ACCUM is for wgrad with MXF_GROUPED_OUT_F32", d->flags);
+  if (!offs) return fail(MXF_E_NULL, "offs is NULL");
+  if (!aligned4(offs) || !aligned4(status)) return fail(MXF_E_ALIGN, "offs or status is not 4-byte aligned");
+  const bool rows = d->M > 0;  // without rows the operands may be NULL
+  if (rows && (!a || !as)) return fail(MXF_E_NULL, wgrad ? "dy_q or dy_s is NULL" : "x_q or x_s is NULL");
+  if (rows && (!b || !bs)) return fail(MXF_E_NULL, wgrad ? "x_q or x_s is NULL" : "w_q or w_s is NULL");
+  if ((wgrad || rows) && !out) return fail(MXF_E_NULL, wgrad ? "dw is NULL" : "y is NULL");
+  const bool f32 = (d->flags & MXF_GROUPED_OUT_F32) != 0;
+  if ((s = check_operand_ptrs(a, as, wgrad ? "dy" : "x")) != MXF_OK || (s = check_operand_ptrs(b, bs, wgrad ? "x" : "w")) != MXF_OK)
+    return s;
+  if (!aligned_to(out, f32 ? 4 : 2)) return fail(MXF_E_ALIGN, "the output is not aligned to its elements");
+  // (the few-rows kernel's strips of 32 columns, up to two tiles of rows for each expert, are the finest grid)
+  const int64_t ct = wgrad ? (d->K + 127) / 128 : (d->N + 31) / 32;
+  const int64_t rt = wgrad ? d->E * ((d->N + 127) / 128) : d->M / 32 + d->E;
+  if (rt > kMostBlocks / ct)
+    return fail(MXF_E_SHAPE, "E = %d, M = %lld, N = %lld, K = %lld: more than 2^24 tiles", d->E, (long long)d->M,
+                (long long)d->N, (long long)d->K);
+  if ((s = check_device()) != MXF_OK) return s;
+  int ncu = 0;
+  if ((s = cu_count(&ncu)) != MXF_OK) return s;
+  mxf::GroupedMxParams p = {};
+  p.a = (const uint8_t*)a; p.as = (const uint8_t*)as;
+  p.b = (const uint8_t*)b; p.bs = (const uint8_t*)bs;
+  p.c = out;
+  p.offs = offs;
+  p.status = status;
+  p.M = d->M; p.N = d->N; p.K = d->K; p.E = d->E;
+  p.ldc = wgrad ? d->K : d->ldy;
+  p.out_f32 = f32;
+  p.accum = (d->flags & MXF_GROUPED_ACCUM) != 0;
+  const bool a8 = (d->flags & MXF_GROUPED_LEFT_E4M3) != 0;
+  MXF_HIP(timed(name, (hipStream_t)stream, [&] { return mxf_launch_grouped_mx(wgrad, p, a8, ncu, (hipStream_t)stream); }),
+          "MXFP4 product launch");
+  return MXF_OK;
+}
+
+mxf_status grouped_gemm_mxfp4_fwd(const mxf_grouped_desc* desc, const int32_t* offs, const void* x_q, const void* x_s,
+                                  const void* w_q, const void* w_s, void* y, int32_t* status, void* stream) {
+  g_err.clear();
+  return run_grouped_mx(false, "mxfp4_fwd", desc, offs, x_q, x_s, w_q, w_s, y, status, stream);
+}
+
+mxf_status grouped_gemm_mxfp4_wgrad(const mxf_grouped_desc* desc, const int32_t* offs, const void* dy_q, const void* dy_s,
+                                    const void* x_q, const void* x_s, void* dw, int32_t* status, void* stream) {
+  g_err.clear();
+  return run_grouped_mx(true, "mxfp4_wgrad", desc, offs, dy_q, dy_s, x_q, x_s, dw, status, stream);
 }
 
 mxf_status mxf_read_status(const void* workspace, void* stream, int32_t* device_status) {

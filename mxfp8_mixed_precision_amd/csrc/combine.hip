@@ -1,0 +1,285 @@
+// Token rows copied to their experts' rows and back, with the router's weights, and the gradients of both.
+//
+//   dispatch      xe[r] = x[a_r / topk], a_r = row_assign[r]; zeros for a pad row (a_r = -1)
+//   combine       y[t] = sum_k w[t, k] h[row(t, k)], row = assign_row; dropped assignments (-1) add nothing
+//   its gradient  dh[r] = w[a_r] dy[a_r / topk] (zeros for a pad row), dw[t, k] = <dy[t], h[row(t, k)]>
+//
+// combine with all weights 1 is dispatch's gradient. Sums are FP32 in the order of k, rounded once; dw is FP32.
+//
+// All three go by tokens: 8, 16, 32 or 64 lanes own one token (the fewest that hold its row in 16-byte chunks),
+// read its row once and touch the topk rows of its assignments with all loads in flight, where going by rows would
+// read a token's row topk times. Bound by HBM. Pad rows are found by further blocks of the same launch, 16 rows of
+// row_assign to a wavefront.
+//
+// A row's last chunk is taken from its end backwards, over elements that its neighbour has too: both store the same
+// values (the dot products skip them), so any width and alignment goes without a branch. Rows shorter than a chunk
+// go element by element.
+#include "chunk.h"
+#include "kernels.h"
+
+namespace mxf {
+
+constexpr int kPadRows = 16;  // rows of row_assign per wavefront
+
+// The expert row of assignment a, -1 if it has none.
+__device__ __forceinline__ int64_t row_of(const RouteParams& p, int64_t a) {
+  const int32_t r = p.assign_row[a];
+  return r >= 0 && r < p.rows ? r : -1;
+}
+
+__device__ __forceinline__ u32x4_t load_any(const void* p) {
+  u32x4_t v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ void store_any(void* p, u32x4_t v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+}
+
+// Zeros into the pad rows of [first, first + kPadRows); rows of `bytes` bytes, `pitch` apart.
+__device__ __forceinline__ void zero_pads(const RouteParams& p, uint8_t* out, int64_t bytes, int64_t pitch, int64_t first) {
+  const int lane = threadIdx.x & 63;
+  const int64_t end = min<int64_t>(p.offs[p.E], p.rows), n = p.tokens * p.topk;
+  const int64_t r = first + lane;
+  bool pad = false;
+  if (lane < kPadRows && r < end) {
+    const int32_t a = p.row_assign[r];
+    pad = a < 0 || a >= n;
+  }
+  const u32x4_t zero = {0, 0, 0, 0};
+  for (uint64_t m = __ballot(pad); m; m &= m - 1) {
+    uint8_t* o = out + (first + __ffsll((unsigned long long)m) - 1) * pitch;
+    if (bytes >= 16) {
+      for (int64_t c = lane * 16; c < bytes; c += 1024) store_any(o + min<int64_t>(c, bytes - 16), zero);
+    } else if (lane < bytes) {
+      o[lane] = 0;
+    }
+  }
+}
+
+// LPT lanes per token.
+template <int LPT>
+__global__ __launch_bounds__(256) void dispatch_kernel(RouteParams p, unsigned token_blocks) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* out = reinterpret_cast<uint8_t*>(p.h);
+  if (blockIdx.x >= token_blocks) {
+    zero_pads(p, out, p.D, p.ldh, ((int64_t)(blockIdx.x - token_blocks) * 4 + wave) * kPadRows);
+    return;
+  }
+  int64_t t = ((int64_t)blockIdx.x * 4 + wave) * (64 / LPT);
+  if (LPT < 64) t += lane / LPT;
+  if (t >= p.tokens) return;
+  const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) + t * p.ldx;
+  const int l = lane % LPT;
+  const int64_t a0 = t * p.topk;
+  if (p.D < 16) {
+    for (int k = 0; k < p.topk; ++k) {
+      const int64_t r = row_of(p, a0 + k);
+      if (r >= 0)
+        for (int64_t c = l; c < p.D; c += LPT) out[r * p.ldh + c] = x[c];
+    }
+    return;
+  }
+  for (int64_t c = l * 16; c < p.D; c += LPT * 16) {
+    const int64_t cc = min<int64_t>(c, p.D - 16);
+    const u32x4_t v = load_any(x + cc);
+    for (int k = 0; k < p.topk; ++k) {
+      const int64_t r = row_of(p, a0 + k);
+      if (r >= 0) store_any(out + r * p.ldh + cc, v);
+    }
+  }
+}
+
+__device__ __forceinline__ float weight_of(const RouteParams& p, int64_t a) {
+  return p.w_f32 ? reinterpret_cast<const float*>(p.w)[a] : Elem<uint16_t>::get(reinterpret_cast<const uint16_t*>(p.w)[a]);
+}
+
+constexpr int kRowsInFlight = 8;
+
+template <class T, int LPT, bool W>
+__global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) {
+  constexpr int VEC = Elem<T>::VEC;
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = LPT == 64 ? wave / spans : wave * (64 / LPT) + lane / LPT;
+  if (t >= p.tokens) return;
+  const T* h = reinterpret_cast<const T*>(p.h);
+  T* y = reinterpret_cast<T*>(p.y) + t * p.ldx;
+  const int64_t a0 = t * p.topk;
+  const int64_t c0 = LPT == 64 ? (wave % spans) * 64 * VEC + lane * VEC : (lane % LPT) * VEC;
+  if (p.D < VEC) {
+    const int64_t c = c0 / VEC;
+    if (c < p.D) {
+      float s = 0.0f;
+      for (int k = 0; k < p.topk; ++k) {
+        const int64_t r = row_of(p, a0 + k);
+        if (r >= 0) s += (W ? weight_of(p, a0 + k) : 1.0f) * Elem<T>::get(h[r * p.ldh + c]);
+      }
+      y[c] = Elem<T>::put(s);
+    }
+    return;
+  }
+  if (c0 >= p.D) return;
+  const int64_t c = min<int64_t>(c0, p.D - VEC);
+  float sum[VEC] = {};
+  for (int k0 = 0; k0 < p.topk; k0 += kRowsInFlight) {
+    u32x4_t v[kRowsInFlight];
+    float w[kRowsInFlight];
+    bool in[kRowsInFlight];
+#pragma unroll
+    for (int k = 0; k < kRowsInFlight; ++k) {
+      const int64_t a = a0 + min(k0 + k, p.topk - 1);
+      const int64_t r = row_of(p, a);
+      in[k] = k0 + k < p.topk && r >= 0;
+      w[k] = W ? weight_of(p, a) : 1.0f;
+      v[k] = (u32x4_t){0, 0, 0, 0};
+      if (in[k]) v[k] = load_any(h + r * p.ldh + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsInFlight; ++k) {
+      if (!in[k]) continue;
+      float f[VEC];
+      Elem<T>::unpack(v[k], f);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) sum[i] = W ? fmaf(w[k], f[i], sum[i]) : sum[i] + f[i];
+    }
+  }
+  store_any(y + c, Elem<T>::pack(sum));
+}
+
+template <class T, int LPT>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigned token_blocks) {
+  constexpr int VEC = Elem<T>::VEC;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (blockIdx.x >= token_blocks) {
+    zero_pads(p, reinterpret_cast<uint8_t*>(p.dh), p.D * sizeof(T), p.lddh * sizeof(T),
+              ((int64_t)(blockIdx.x - token_blocks) * 4 + wave) * kPadRows);
+    return;
+  }
+  int64_t t = ((int64_t)blockIdx.x * 4 + wave) * (64 / LPT);
+  if (LPT < 64) t += lane / LPT;
+  const bool live = t < p.tokens;
+  if (LPT == 64 && !live) return;
+  const int l = lane % LPT;
+  const T* dy = reinterpret_cast<const T*>(p.dy) + (live ? t : 0) * p.ldx;
+  const T* h = reinterpret_cast<const T*>(p.h);
+  T* dh = reinterpret_cast<T*>(p.dh);
+  const int64_t a0 = t * p.topk;
+  for (int k0 = 0; k0 < p.topk; k0 += kRowsInFlight) {
+    float w[kRowsInFlight], dot[kRowsInFlight];
+    int64_t row[kRowsInFlight];
+#pragma unroll
+    for (int k = 0; k < kRowsInFlight; ++k) {
+      const bool in = live && k0 + k < p.topk;
+      row[k] = in ? row_of(p, a0 + k0 + k) : -1;
+      w[k] = row[k] >= 0 ? weight_of(p, a0 + k0 + k) : 0.0f;
+      dot[k] = 0.0f;
+    }
+    if (p.D < VEC) {
+      for (int64_t c = l; c < p.D; c += LPT) {
+        const float g = Elem<T>::get(dy[c]);
+#pragma unroll
+        for (int k = 0; k < kRowsInFlight; ++k)
+          if (row[k] >= 0) {
+            dot[k] = fmaf(g, Elem<T>::get(h[row[k] * p.ldh + c]), dot[k]);
+            dh[row[k] * p.lddh + c] = Elem<T>::put(w[k] * g);
+          }
+      }
+    } else {
+      for (int64_t c0 = l * VEC; c0 < p.D; c0 += LPT * VEC) {
+        const int64_t c = min<int64_t>(c0, p.D - VEC);
+        const int skip = (int)(c0 - c);  // elements that the chunk before has too
+        const u32x4_t gv = load_any(dy + c);
+        u32x4_t v[kRowsInFlight];
+#pragma unroll
+        for (int k = 0; k < kRowsInFlight; ++k)
+          if (row[k] >= 0) v[k] = load_any(h + row[k] * p.ldh + c);
+        float g[VEC];
+        Elem<T>::unpack(gv, g);
+#pragma unroll
+        for (int k = 0; k < kRowsInFlight; ++k) {
+          if (row[k] < 0) continue;
+          float f[VEC], o[VEC];
+          Elem<T>::unpack(v[k], f);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            o[i] = w[k] * g[i];
+            dot[k] = i < skip ? dot[k] : fmaf(g[i], f[i], dot[k]);
+          }
+          store_any(dh + row[k] * p.lddh + c, Elem<T>::pack(o));
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsInFlight; ++k) {
+      float s = dot[k];
+#pragma unroll
+      for (int o = LPT / 2; o; o >>= 1) s += __shfl_xor(s, o);
+      if (l == 0 && live && k0 + k < p.topk) p.dw[a0 + k0 + k] = s;
+    }
+  }
+}
+
+}  // namespace mxf
+
+namespace {
+
+// Lanes that hold a row of `chunks` 16-byte chunks: a power of two from 8 to 64.
+int lanes_per_token(int64_t chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64; }
+unsigned blocks_of(int64_t waves) { return (unsigned)((waves + 3) / 4); }
+unsigned pad_blocks(int64_t rows) { return blocks_of((rows + mxf::kPadRows - 1) / mxf::kPadRows); }
+
+template <class Fn>
+hipError_t with_lanes(int64_t chunks, Fn&& fn) {
+  switch (lanes_per_token(chunks)) {
+    case 8: return fn(std::integral_constant<int, 8>());
+    case 16: return fn(std::integral_constant<int, 16>());
+    case 32: return fn(std::integral_constant<int, 32>());
+    default: return fn(std::integral_constant<int, 64>());
+  }
+}
+
+template <class T, bool W>
+hipError_t launch_combine(const mxf::RouteParams& p, hipStream_t st) {
+  const int64_t chunks = (p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC;
+  const int64_t spans = (chunks + 63) / 64;
+  return with_lanes(chunks, [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    const int64_t waves = L == 64 ? p.tokens * spans : (p.tokens + 64 / L - 1) / (64 / L);
+    hipLaunchKernelGGL((mxf::combine_kernel<T, L, W>), dim3(blocks_of(waves)), dim3(256), 0, st, p, (int)spans);
+    return hipGetLastError();
+  });
+}
+
+template <class T>
+hipError_t launch_combine_bwd(const mxf::RouteParams& p, hipStream_t st) {
+  return with_lanes((p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC, [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    const unsigned tb = blocks_of((p.tokens + 64 / L - 1) / (64 / L));
+    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L>), dim3(tb + pad_blocks(p.rows)), dim3(256), 0, st, p, tb);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+// D, ldx and ldh in bytes.
+hipError_t mxf_launch_dispatch(const mxf::RouteParams& p, hipStream_t st) {
+  return with_lanes((p.D + 15) / 16, [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    const unsigned tb = blocks_of((p.tokens + 64 / L - 1) / (64 / L));
+    const unsigned n = tb + pad_blocks(p.rows);
+    if (n == 0) return hipSuccess;
+    hipLaunchKernelGGL((mxf::dispatch_kernel<L>), dim3(n), dim3(256), 0, st, p, tb);
+    return hipGetLastError();
+  });
+}
+
+hipError_t mxf_launch_combine(const mxf::RouteParams& p, bool f32, hipStream_t st) {
+  if (p.w) return f32 ? launch_combine<float, true>(p, st) : launch_combine<uint16_t, true>(p, st);
+  return f32 ? launch_combine<float, false>(p, st) : launch_combine<uint16_t, false>(p, st);
+}
+
+hipError_t mxf_launch_combine_bwd(const mxf::RouteParams& p, bool f32, hipStream_t st) {
+  return f32 ? launch_combine_bwd<float>(p, st) : launch_combine_bwd<uint16_t>(p, st);
+}

@@ -20,77 +20,13 @@
 #include "chunk.h"
 #include "kernels.h"
 #include "mx_device.h"
+#include "ragged.h"
 
 namespace mxf {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// The contract of offs (offs[0] = 0, non-decreasing, offs[E] <= M), the number of row tiles of all
-// experts, and the expert and rows of row tile t. Whole wavefronts, the same answer in every lane:
-// lane i looks at expert 64 j + i, tiles are counted in expert order. Offsets that break the contract may
-// leave any counts behind; the caller stops on ok = false before it uses them.
-struct RowTile {
-  int e;       // -1: past the last tile
-  int m0, m1;  // rows of the tile
-};
-struct RowTiles {
-  bool ok;
-  int tiles;
-  int lo, hi, first, n;  // of the lane's last expert looked at (E <= 64: its only one)
-};
-__device__ __forceinline__ void scan_experts(const int32_t* offs, int E, int bm, int base, RowTiles& r) {
-  const int lane = threadIdx.x & 63, i = base + lane;
-  r.lo = i < E ? offs[i] : 0;
-  r.hi = i < E ? offs[i + 1] : 0;
-  r.n = r.hi > r.lo ? (int)(((uint32_t)r.hi - (uint32_t)r.lo + bm - 1) / bm) : 0;
-  int pre = r.n;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(pre, o);
-    if (lane >= o) pre += v;
-  }
-  r.first = r.tiles + pre - r.n;
-  r.tiles += __builtin_amdgcn_readlane(pre, 63);
-}
-__device__ __forceinline__ RowTiles count_row_tiles(const int32_t* offs, int E, int64_t M, int bm) {
-  RowTiles r = {true, 0, 0, 0, 0, 0};
-  bool bad = false;
-  for (int base = 0; base < E; base += 64) {
-    scan_experts(offs, E, bm, base, r);
-    bad = bad || r.lo > r.hi || r.lo < 0 || r.hi > M || (base == 0 && (threadIdx.x & 63) == 0 && r.lo != 0);
-  }
-  r.ok = !__any(bad);
-  return r;
-}
-__device__ __forceinline__ RowTile find_row_tile(RowTiles r, const int32_t* offs, int E, int bm, int t) {
-  if (E > 64) r.tiles = 0;
-  for (int base = 0; base < E; base += 64) {
-    if (E > 64) scan_experts(offs, E, bm, base, r);
-    const uint64_t hit = __ballot(r.n > 0 && t >= r.first && t < r.first + r.n);
-    if (hit) {
-      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-      const int m0 = __builtin_amdgcn_readlane(r.lo, l) + (t - __builtin_amdgcn_readlane(r.first, l)) * bm;
-      return {base + l, m0, min(m0 + bm, __builtin_amdgcn_readlane(r.hi, l))};
-    }
-  }
-  return {-1, 0, 0};
-}
-
-// The contract alone.
-__device__ __forceinline__ bool ragged_ok(const int32_t* offs, int E, int64_t M) {
-  bool bad = false;
-  for (int i = threadIdx.x & 63; i < E; i += 64) {
-    const int32_t lo = offs[i], hi = offs[i + 1];
-    if (lo > hi || lo < 0 || hi > M || (i == 0 && lo != 0)) bad = true;
-  }
-  return !__any(bad);
-}
-
-__device__ __forceinline__ float e8m0_value(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte ? byte << 23 : 0x00400000u);
-}
 
 // ------------------------------------------------------------------ pipelined tiles
 
@@ -122,22 +58,9 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
 // element; a lane whose row or column does not exist asks for an offset past it and gets zeros in
 // LDS. So ragged segment ends, odd tile ends and the last contraction stage need no other path, rows of
 // another expert are never read, and 64-bit offsets live in the descriptor's base.
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr uint32_t kNoElement = 0x80000000u;  // = the descriptors' size
-
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
-         ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
-}
-// 16 bytes per lane into LDS [lds, lds + 1024) in lane order. The loads have no destination registers;
-// the kernel waits for them with vmcnt. (One wait state between a write of M0 and its use.)
-__device__ __forceinline__ void buffer_to_lds(i32x4 rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
-               : "memory", "m0");
-}
 // One operand of a tile: R rows or columns of the output, contraction-contiguous (KC) or not.
 template <bool KC, int R>
 struct Operand {
@@ -684,12 +607,6 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& p, uint8_t* sm
   }
 }
 
-// Position of block b of n (a contiguous run of positions per XCD: blocks go to the 8 XCDs in turn).
-__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
-  const uint32_t q = n / 8, r = n % 8, x = b % 8;
-  return (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + b / 8;
-}
-
 // OP 0 and 1: row tiles in groups of GM, all column tiles of a group before the next, so that the tiles
 // in flight on an XCD share rows of x and columns of w in its L2.
 //
@@ -765,23 +682,8 @@ __global__ __launch_bounds__(256, !RING ? 4 : BM == 256 ? 1 : 2) void grouped_dw
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = ok ? 0 : 1;
   if (!ok) return;
   const uint32_t per = (uint32_t)row_tiles * (uint32_t)col_tiles;
-  const int place = (int)(blockIdx.x / per);
-  int e = __builtin_amdgcn_readfirstlane(place), c0, c1;
-  if (p.E <= 64) {
-    const int lane = threadIdx.x & 63;
-    const int lo = lane < p.E ? p.offs[lane] : 0, hi = lane < p.E ? p.offs[lane + 1] : -1, n = hi - lo;
-    int rank = 0;
-    for (int j = 0; j < p.E; ++j) {
-      const int nj = __builtin_amdgcn_readlane(n, j);
-      rank += nj > n || (nj == n && j < lane);
-    }
-    e = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(lane < p.E && rank == place)) - 1);
-    c0 = __builtin_amdgcn_readlane(lo, e);
-    c1 = __builtin_amdgcn_readlane(hi, e);
-  } else {
-    c0 = p.offs[e];
-    c1 = p.offs[e + 1];
-  }
+  const Segment sg = by_length(p.offs, p.E, (int)(blockIdx.x / per));
+  const int e = sg.e, c0 = sg.lo, c1 = sg.hi;
   const uint32_t pos = xcd_run(blockIdx.x % per, per);
   // (row tiles in groups, as above)
   constexpr uint32_t GM = 4;

@@ -79,8 +79,66 @@ struct GroupedParams {
   int out_f32, accum;
 };
 
+// Token rows to their experts' rows and back (combine.hip). Strides in elements (dispatch: bytes).
+struct RouteParams {
+  const int32_t* offs;        // [E + 1], read where pad rows are written
+  const int32_t* row_assign;  // [rows]
+  const int32_t* assign_row;  // [tokens * topk]
+  int E, topk;
+  int64_t tokens, rows, D;
+  int64_t ldx, ldh, lddh;     // token rows (x, y, dy); expert rows (h, and xe of dispatch); dh
+  const void* x;
+  const void* dy;
+  const void* w;              // [tokens, topk], null: 1
+  bool w_f32;
+  void* h;                    // combine and its gradient: read; dispatch: xe, written
+  void* y;
+  void* dh;
+  float* dw;                  // [tokens, topk]
+};
+
+// MXFP4 operands (mxfp4.hip). A matrix [rows, K] is held as code panels [ceil(K/128)][rows][64] of E2M1 pairs (E4M3:
+// [2 ceil(K/128)][rows][64] bytes) and scale planes [ceil(K/128)][rows][4]; `batch` matrices one after another.
+struct Mx4Params {
+  const void* x;              // [batch][rows, cols], row stride ldx, batch stride xs
+  void* out;                  // dequantise: [batch][rows, cols], dense
+  uint8_t* q;                 // along rows (null: not wanted)
+  uint8_t* s;
+  uint8_t* qt;                // along columns: the operand of the transposed matrix
+  uint8_t* st;
+  int64_t batch, rows, cols, ldx, xs;
+  const int32_t* row_assign;  // null: rows as they are; else row r is token row_assign[r] / topk of `tokens`, or zeros
+  const int32_t* offs;
+  int E, topk;
+  int64_t tokens;
+};
+
+// Expert products on MXFP4 operands (grouped_mx.hip). Left operand a (E2M1, or E4M3 with a8), right operand b.
+struct GroupedMxParams {
+  const uint8_t* a;
+  const uint8_t* as;
+  const uint8_t* b;
+  const uint8_t* bs;
+  void* c;
+  const int32_t* offs;
+  int32_t* status;    // may be null
+  int64_t M, N, K;    // as GroupedParams
+  int64_t ldc;
+  int E;
+  int out_f32, accum;
+};
+
 }  // namespace mxf
 
+// combine.hip
+hipError_t mxf_launch_dispatch(const mxf::RouteParams& p, hipStream_t st);
+hipError_t mxf_launch_combine(const mxf::RouteParams& p, bool f32, hipStream_t st);
+hipError_t mxf_launch_combine_bwd(const mxf::RouteParams& p, bool f32, hipStream_t st);
+// mxfp4.hip
+hipError_t mxf_launch_mxfp4_quantize(const mxf::Mx4Params& p, bool f32, bool e4m3, hipStream_t st);
+hipError_t mxf_launch_mxfp4_dequantize(const mxf::Mx4Params& p, bool f32, bool e4m3, hipStream_t st);
+// grouped_mx.hip
+hipError_t mxf_launch_grouped_mx(bool wgrad, const mxf::GroupedMxParams& p, bool a8, int ncu, hipStream_t st);
 // norm.hip
 int mxf_norm_parts(int64_t rows, int64_t cols);
 hipError_t mxf_launch_norm_fwd(const mxf::NormParams& p, bool f32, hipStream_t st);
