@@ -133,7 +133,7 @@ def lib():
             "grouped_gemm_dgrad": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp]),
             "grouped_gemm_wgrad": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), vp, vp, vp, vp, vp, vp, vp, vp]),
             "mxf_dispatch_fwd": (ctypes.c_int, [ctypes.POINTER(RouteDesc), vp, vp, vp, vp, vp, vp]),
-            "mxf_combine_fwd": (ctypes.c_int, [ctypes.POINTER(RouteDesc), vp, vp, vp, vp, vp]),
+            "mxf_combine_fwd": (ctypes.c_int, [ctypes.POINTER(RouteDesc), vp, vp, vp, vp, vp, vp]),
             "mxf_combine_bwd": (ctypes.c_int, [ctypes.POINTER(RouteDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "mxfp4_quantize": (ctypes.c_int, [ctypes.POINTER(OperandDesc), vp, vp, vp, vp, vp, vp, vp, vp]),
             "mxfp4_dequantize": (ctypes.c_int, [ctypes.POINTER(OperandDesc), vp, vp, vp, vp]),
@@ -405,9 +405,9 @@ def mxf_dispatch_fwd(desc, offs, row_assign, assign_row, x, xe, stream=None):
                                   _stream(stream)))
 
 
-def mxf_combine_fwd(desc, assign_row, h, weights, y, stream=None):
+def mxf_combine_fwd(desc, assign_row, h, weights, residual, y, stream=None):
     """Raw call: pointers (tensors or ints) and a RouteDesc, as in the C header."""
-    _check(lib().mxf_combine_fwd(ctypes.byref(desc), _ptr(assign_row), _ptr(h), _ptr(weights), _ptr(y),
+    _check(lib().mxf_combine_fwd(ctypes.byref(desc), _ptr(assign_row), _ptr(h), _ptr(weights), _ptr(residual), _ptr(y),
                                  _stream(stream)))
 
 

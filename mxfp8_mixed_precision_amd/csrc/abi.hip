@@ -963,21 +963,25 @@ mxf_status mxf_dispatch_fwd(const mxf_route_desc* d, const int32_t* offs, const 
 }
 
 mxf_status mxf_combine_fwd(const mxf_route_desc* d, const int32_t* assign_row, const void* h, const void* weights,
-                           void* y, void* stream) {
+                           const void* residual, void* y, void* stream) {
   g_err.clear();
   mxf_status st = check_route_desc(d, MXF_ROUTE_F32 | MXF_ROUTE_WEIGHT_F32);
   if (st != MXF_OK) return st;
+  if (residual && d->lddh < d->D)
+    return fail(MXF_E_SHAPE, "lddh = %lld: must be at least D (%lld)", (long long)d->lddh, (long long)d->D);
   if (d->tokens == 0) return MXF_OK;
   const bool f32 = (d->flags & MXF_ROUTE_F32) != 0;
   const size_t n = f32 ? 4 : 2;
   if (!assign_row || !y || (d->rows > 0 && !h)) return fail(MXF_E_NULL, "assign_row, h or y is NULL");
   if (!aligned4(assign_row)) return fail(MXF_E_ALIGN, "assign_row is not 4-byte aligned");
-  if (!aligned_to(h, n) || !aligned_to(y, n) || !aligned_to(weights, (d->flags & MXF_ROUTE_WEIGHT_F32) ? 4 : 2))
-    return fail(MXF_E_ALIGN, "h, y or weights is not aligned to its elements");
+  if (!aligned_to(h, n) || !aligned_to(y, n) || !aligned_to(residual, n) ||
+      !aligned_to(weights, (d->flags & MXF_ROUTE_WEIGHT_F32) ? 4 : 2))
+    return fail(MXF_E_ALIGN, "h, y, residual or weights is not aligned to its elements");
   if ((st = check_device()) != MXF_OK) return st;
   mxf::RouteParams p = route_params(d);
   p.assign_row = assign_row;
   p.h = const_cast<void*>(h); p.w = weights; p.y = y;
+  p.residual = residual; p.ldr = d->lddh;
   MXF_HIP(timed("combine_fwd", (hipStream_t)stream, [&] { return mxf_launch_combine(p, f32, (hipStream_t)stream); }),
           "combine launch");
   return MXF_OK;
@@ -994,8 +998,8 @@ mxf_status mxf_combine_bwd(const mxf_route_desc* d, const int32_t* offs, const i
   if ((st = check_route_maps(d, offs, row_assign, assign_row)) != MXF_OK) return st;
   const bool f32 = (d->flags & MXF_ROUTE_F32) != 0;
   const size_t n = f32 ? 4 : 2;
-  if (d->tokens > 0 && (!dy || !weights || !dweights)) return fail(MXF_E_NULL, "dy, weights or dweights is NULL");
-  if (d->rows > 0 && (!h || !dh)) return fail(MXF_E_NULL, "h or dh is NULL");
+  if (d->tokens > 0 && (!dy || !weights)) return fail(MXF_E_NULL, "dy or weights is NULL");
+  if (d->rows > 0 && ((dweights && !h) || !dh)) return fail(MXF_E_NULL, "h or dh is NULL");
   if (!aligned_to(dy, n) || !aligned_to(h, n) || !aligned_to(dh, n) || !aligned4(dweights) ||
       !aligned_to(weights, (d->flags & MXF_ROUTE_WEIGHT_F32) ? 4 : 2))
     return fail(MXF_E_ALIGN, "dy, h, dh, weights or dweights is not aligned to its elements");

@@ -1,7 +1,7 @@
 // Token rows copied to their experts' rows and back, with the router's weights, and the gradients of both.
 //
 //   dispatch      xe[r] = x[a_r / topk], a_r = row_assign[r]; zeros for a pad row (a_r = -1)
-//   combine       y[t] = sum_k w[t, k] h[row(t, k)], row = assign_row; dropped assignments (-1) add nothing
+//   combine       y[t] = (residual[t] +) sum_k w[t, k] h[row(t, k)], row = assign_row; dropped assignments (-1) add nothing
 //   its gradient  dh[r] = w[a_r] dy[a_r / topk] (zeros for a pad row), dw[t, k] = <dy[t], h[row(t, k)]>
 //
 // combine with all weights 1 is dispatch's gradient. Sums are FP32 in the order of k, rounded once; dw is FP32.
@@ -105,12 +105,13 @@ __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) 
   if (t >= p.tokens) return;
   const T* h = reinterpret_cast<const T*>(p.h);
   T* y = reinterpret_cast<T*>(p.y) + t * p.ldx;
+  const T* res = p.residual ? reinterpret_cast<const T*>(p.residual) + t * p.ldr : nullptr;
   const int64_t a0 = t * p.topk;
   const int64_t c0 = LPT == 64 ? (wave % spans) * 64 * VEC + lane * VEC : (lane % LPT) * VEC;
   if (p.D < VEC) {
     const int64_t c = c0 / VEC;
     if (c < p.D) {
-      float s = 0.0f;
+      float s = res ? Elem<T>::get(res[c]) : 0.0f;
       for (int k = 0; k < p.topk; ++k) {
         const int64_t r = row_of(p, a0 + k);
         if (r >= 0) s += (W ? weight_of(p, a0 + k) : 1.0f) * Elem<T>::get(h[r * p.ldh + c]);
@@ -122,6 +123,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) 
   if (c0 >= p.D) return;
   const int64_t c = min<int64_t>(c0, p.D - VEC);
   float sum[VEC] = {};
+  if (res) Elem<T>::unpack(load_any(res + c), sum);
   for (int k0 = 0; k0 < p.topk; k0 += kRowsInFlight) {
     u32x4_t v[kRowsInFlight];
     float w[kRowsInFlight];
@@ -147,7 +149,8 @@ __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) 
   store_any(y + c, Elem<T>::pack(sum));
 }
 
-template <class T, int LPT>
+// DOT: the weights' gradient too; without it h is not read.
+template <class T, int LPT, bool DOT>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigned token_blocks) {
   constexpr int VEC = Elem<T>::VEC;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -181,7 +184,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigne
 #pragma unroll
         for (int k = 0; k < kRowsInFlight; ++k)
           if (row[k] >= 0) {
-            dot[k] = fmaf(g, Elem<T>::get(h[row[k] * p.ldh + c]), dot[k]);
+            if (DOT) dot[k] = fmaf(g, Elem<T>::get(h[row[k] * p.ldh + c]), dot[k]);
             dh[row[k] * p.lddh + c] = Elem<T>::put(w[k] * g);
           }
       }
@@ -193,23 +196,24 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigne
         u32x4_t v[kRowsInFlight];
 #pragma unroll
         for (int k = 0; k < kRowsInFlight; ++k)
-          if (row[k] >= 0) v[k] = load_any(h + row[k] * p.ldh + c);
+          if (DOT && row[k] >= 0) v[k] = load_any(h + row[k] * p.ldh + c);
         float g[VEC];
         Elem<T>::unpack(gv, g);
 #pragma unroll
         for (int k = 0; k < kRowsInFlight; ++k) {
           if (row[k] < 0) continue;
           float f[VEC], o[VEC];
-          Elem<T>::unpack(v[k], f);
+          if (DOT) Elem<T>::unpack(v[k], f);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             o[i] = w[k] * g[i];
-            dot[k] = i < skip ? dot[k] : fmaf(g[i], f[i], dot[k]);
+            if (DOT) dot[k] = i < skip ? dot[k] : fmaf(g[i], f[i], dot[k]);
           }
           store_any(dh + row[k] * p.lddh + c, Elem<T>::pack(o));
         }
       }
     }
+    if constexpr (!DOT) continue;
 #pragma unroll
     for (int k = 0; k < kRowsInFlight; ++k) {
       float s = dot[k];
@@ -251,12 +255,12 @@ hipError_t launch_combine(const mxf::RouteParams& p, hipStream_t st) {
   });
 }
 
-template <class T>
+template <class T, bool DOT>
 hipError_t launch_combine_bwd(const mxf::RouteParams& p, hipStream_t st) {
   return with_lanes((p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
     const unsigned tb = blocks_of((p.tokens + 64 / L - 1) / (64 / L));
-    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L>), dim3(tb + pad_blocks(p.rows)), dim3(256), 0, st, p, tb);
+    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L, DOT>), dim3(tb + pad_blocks(p.rows)), dim3(256), 0, st, p, tb);
     return hipGetLastError();
   });
 }
@@ -281,5 +285,6 @@ hipError_t mxf_launch_combine(const mxf::RouteParams& p, bool f32, hipStream_t s
 }
 
 hipError_t mxf_launch_combine_bwd(const mxf::RouteParams& p, bool f32, hipStream_t st) {
-  return f32 ? launch_combine_bwd<float>(p, st) : launch_combine_bwd<uint16_t>(p, st);
+  if (p.dw) return f32 ? launch_combine_bwd<float, true>(p, st) : launch_combine_bwd<uint16_t, true>(p, st);
+  return f32 ? launch_combine_bwd<float, false>(p, st) : launch_combine_bwd<uint16_t, false>(p, st);
 }

@@ -86,15 +86,16 @@ struct RouteParams {
   const int32_t* assign_row;  // [tokens * topk]
   int E, topk;
   int64_t tokens, rows, D;
-  int64_t ldx, ldh, lddh;     // token rows (x, y, dy); expert rows (h, and xe of dispatch); dh
+  int64_t ldx, ldh, lddh, ldr;  // token rows (x, y, dy); expert rows (h, and xe of dispatch); dh; residual
   const void* x;
   const void* dy;
   const void* w;              // [tokens, topk], null: 1
+  const void* residual;       // added to y, may be null
   bool w_f32;
   void* h;                    // combine and its gradient: read; dispatch: xe, written
   void* y;
   void* dh;
-  float* dw;                  // [tokens, topk]
+  float* dw;                  // [tokens, topk], null: not wanted, and h is not read
 };
 
 // MXFP4 operands (mxfp4.hip). A matrix [rows, K] is held as code panels [ceil(K/128)][rows][64] of E2M1 pairs (E4M3:

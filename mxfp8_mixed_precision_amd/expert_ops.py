@@ -66,7 +66,7 @@ def dispatch_fwd(x, plan):
     return xe
 
 
-def _combine(h, weights, plan, tokens):
+def _combine(h, weights, plan, tokens, residual=None):
     torch = _t()
     rows, D, ld = _rows(h, "h")
     dev = h.device
@@ -75,10 +75,16 @@ def _combine(h, weights, plan, tokens):
     flags = _float_flag(h, "h")
     if weights is not None:
         flags |= 2 * _float_flag(weights, "weights")
-        _dense(weights, (tokens, topk), weights.dtype, dev, "weights")
+        _dense(weights, (tokens, topk if tokens else weights.shape[1]), weights.dtype, dev, "weights")
+    ldr = D
+    if residual is not None:
+        if residual.dtype != h.dtype or tuple(residual.shape) != (tokens, D):
+            _bad(f"residual: a {h.dtype} tensor [{tokens}, {D}] is needed")
+        _on(residual, dev, "residual")
+        ldr = _rows(residual, "residual")[2]
     y = torch.empty((tokens, D), dtype=h.dtype, device=dev)
-    _run("mxf_combine_fwd", RouteDesc(tokens, rows, D, D, ld, D, topk, offs.numel() - 1, 0, flags), assign_row.data_ptr(),
-         h.data_ptr(), _ptr(weights), y.data_ptr(), _stream_of(dev))
+    _run("mxf_combine_fwd", RouteDesc(tokens, rows, D, D, ld, ldr, topk, offs.numel() - 1, 0, flags), assign_row.data_ptr(),
+         h.data_ptr(), _ptr(weights), _ptr(residual), y.data_ptr(), _stream_of(dev))
     return y
 
 
@@ -89,34 +95,38 @@ def dispatch_bwd(dxe, plan, tokens):
 
 
 @_on_stream
-def combine_fwd(h, weights, plan):
-    """y [tokens, D]: each token's rows of h [rows, D] (BF16 or FP32) times weights [tokens, topk] (BF16 or FP32), added up."""
+def combine_fwd(h, weights, plan, residual=None):
+    """y [tokens, D]: each token's rows of h [rows, D] (BF16 or FP32) times weights [tokens, topk] (BF16 or FP32), added up,
+    and onto residual [tokens, D] if there is one (of h's type; y is rounded once)."""
     if weights is None or weights.dim() != 2:
         _bad("weights [tokens, topk] are needed")
-    return _combine(h, weights, plan, weights.shape[0])
+    return _combine(h, weights, plan, weights.shape[0], residual)
 
 
 @_on_stream
 def combine_bwd(dy, h, weights, plan):
-    """(dh, dweights) of combine_fwd: dh [rows, D] like h, zeros in pad rows, and dweights [tokens, topk] FP32."""
+    """(dh, dweights) of combine_fwd: dh [rows, D] like dy, zeros in pad rows, and dweights [tokens, topk] FP32 (None where h
+    is None: h is only needed for it)."""
     torch = _t()
     tokens, D, ldy = _rows(dy, "dy")
-    rows, Dh, ldh = _rows(h, "h")
     dev = dy.device
-    if Dh != D or h.dtype != dy.dtype:
-        _bad("h and dy differ in type or width")
-    _on(h, dev, "h")
+    rows, ldh = None, D
+    if h is not None:
+        rows, Dh, ldh = _rows(h, "h")
+        if Dh != D or h.dtype != dy.dtype:
+            _bad("h and dy differ in type or width")
+        _on(h, dev, "h")
     offs, row_assign, assign_row = _plan(plan, dev, rows)
-    topk = _topk(assign_row, tokens)
-    if weights is None:
+    rows, topk = row_assign.numel(), _topk(assign_row, tokens)
+    if weights is None or weights.dim() != 2:
         _bad("weights [tokens, topk] are needed")
     flags = _float_flag(dy, "dy") | 2 * _float_flag(weights, "weights")
-    _dense(weights, (tokens, topk) if tokens else tuple(weights.shape), weights.dtype, dev, "weights")
-    dh = torch.empty((rows, D), dtype=h.dtype, device=dev)
-    dw = torch.empty(tuple(weights.shape), dtype=torch.float32, device=dev)
+    _dense(weights, (tokens, topk if tokens else weights.shape[1]), weights.dtype, dev, "weights")
+    dh = torch.empty((rows, D), dtype=dy.dtype, device=dev)
+    dw = torch.empty(tuple(weights.shape), dtype=torch.float32, device=dev) if h is not None else None
     _run("mxf_combine_bwd", RouteDesc(tokens, rows, D, ldy, ldh, D, topk, offs.numel() - 1, 0, flags), offs.data_ptr(),
-         row_assign.data_ptr(), assign_row.data_ptr(), dy.data_ptr(), h.data_ptr(), weights.data_ptr(), dh.data_ptr(),
-         dw.data_ptr(), _stream_of(dev))
+         row_assign.data_ptr(), assign_row.data_ptr(), dy.data_ptr(), _ptr(h), weights.data_ptr(), dh.data_ptr(), _ptr(dw),
+         _stream_of(dev))
     return dh, dw
 
 
