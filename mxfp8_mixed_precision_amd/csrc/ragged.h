@@ -104,15 +104,21 @@ __device__ __forceinline__ void buffer_to_lds(i32x4 rsrc, uint32_t voff, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
-// 4 bytes per lane into LDS [lds, lds + 256).
+// The same with OFF (a constant) more on both sides, and 4 bytes per lane into LDS [lds, lds + 256).
+template <int OFF>
+__device__ __forceinline__ void buffer_to_lds_off(i32x4 rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 lds" ::"s"(lds), "v"(voff),
+               "s"(rsrc), "i"(OFF)
+               : "memory", "m0");
+}
 __device__ __forceinline__ void buffer_to_lds4(i32x4 rsrc, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
-// A descriptor of [base, base + 2 GB), and the same moved on. (48-bit addresses: no stride bits.)
-__device__ __forceinline__ i32x4 descriptor(const void* p) {
+// A descriptor of [p, p + bytes), and the same moved on. (48-bit addresses: no stride bits.)
+__device__ __forceinline__ i32x4 descriptor(const void* p, int bytes = (int)kNoElement) {
   const uint64_t base = uniform64((uint64_t)p);
-  return (i32x4){(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)kNoElement, 0x00020000};
+  return (i32x4){(int)(uint32_t)base, (int)(uint32_t)(base >> 32), __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
 __device__ __forceinline__ void move_on(i32x4& rsrc, uint64_t bytes) {
   const uint64_t b = ((uint64_t)(uint32_t)rsrc[1] << 32 | (uint32_t)rsrc[0]) + bytes;

@@ -130,6 +130,15 @@ def test_forward_of_many_tiles(counts, N, K, e4m3, out):
     check_fwd(counts, N, K, e4m3, out, seed=N, tail=3)
 
 
+# several rounds of the chip's tiles: blocks that walk a list of them (uneven ends, odd numbers of columns of tiles, columns
+# that end inside a piece of 32, one expert, more experts than lanes, contractions of the fewest panels)
+@pytest.mark.parametrize("counts,N,K", [([9000, 0, 7000, 301, 1], 4096, 1000), ([33000], 2056, 897), ([300] * 70 + [5000], 1992, 1024),
+                                        ([2500, 3333, 1, 12000, 4097], 2816, 1536), ([70000], 648, 2048)])
+def test_forward_of_long_lists(counts, N, K):
+    require_gpu()
+    check_fwd(counts, N, K, False, BF, seed=N, tail=3)
+
+
 WCASES = [([1], 1, 1), ([0, 2], 24, 16), ([1, 0, 3], 130, 129), ([2, 2, 1], 256, 320), ([5], 77, 515), ([0, 0], 40, 40), ([1] * 66, 33, 65),
           ([3, 0, 9, 1], 520, 264)]
 
