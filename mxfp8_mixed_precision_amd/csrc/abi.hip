@@ -915,7 +915,7 @@ static mxf_status check_route_desc(const mxf_route_desc* d, uint32_t flags) {
     return fail(MXF_E_SHAPE, "ldx = %lld, ldh = %lld: must be at least D (%lld)", (long long)d->ldx, (long long)d->ldh,
                 (long long)d->D);
   if (d->flags & ~flags) return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
-  if ((d->tokens * ((d->D + 255) / 256) + d->rows / 16) / 4 + 2 > kMostBlocks)
+  if (d->tokens * ((d->D + 127) / 128) / 4 + d->rows / 64 + 2 > kMostBlocks)
     return fail(MXF_E_SHAPE, "tokens = %lld, rows = %lld, D = %lld: too many blocks", (long long)d->tokens,
                 (long long)d->rows, (long long)d->D);
   return MXF_OK;

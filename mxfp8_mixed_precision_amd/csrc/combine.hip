@@ -20,6 +20,7 @@
 namespace mxf {
 
 constexpr int kPadRows = 16;  // rows of row_assign per wavefront
+constexpr int kRowsInFlight = 8;
 
 // The expert row of assignment a, -1 if it has none.
 __device__ __forceinline__ int64_t row_of(const RouteParams& p, int64_t a) {
@@ -57,44 +58,43 @@ __device__ __forceinline__ void zero_pads(const RouteParams& p, uint8_t* out, in
   }
 }
 
-// LPT lanes per token.
+// LPT lanes per token; with 64 a wavefront takes one span of 64 chunks of it.
 template <int LPT>
-__global__ __launch_bounds__(256) void dispatch_kernel(RouteParams p, unsigned token_blocks) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void dispatch_kernel(RouteParams p, unsigned pad_blocks, int spans) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t* out = reinterpret_cast<uint8_t*>(p.h);
-  if (blockIdx.x >= token_blocks) {
-    zero_pads(p, out, p.D, p.ldh, ((int64_t)(blockIdx.x - token_blocks) * 4 + wave) * kPadRows);
+  if (blockIdx.x < pad_blocks) {
+    zero_pads(p, out, p.D, p.ldh, ((int64_t)blockIdx.x * 4 + w) * kPadRows);
     return;
   }
-  int64_t t = ((int64_t)blockIdx.x * 4 + wave) * (64 / LPT);
-  if (LPT < 64) t += lane / LPT;
+  const int64_t wave = (int64_t)(blockIdx.x - pad_blocks) * 4 + w;
+  const int64_t t = LPT == 64 ? wave / spans : wave * (64 / LPT) + lane / LPT;
   if (t >= p.tokens) return;
   const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) + t * p.ldx;
-  const int l = lane % LPT;
-  const int64_t a0 = t * p.topk;
+  const int64_t a0 = t * p.topk, c = LPT == 64 ? (wave % spans) * 1024 + lane * 16 : lane % LPT * 16;
   if (p.D < 16) {
     for (int k = 0; k < p.topk; ++k) {
       const int64_t r = row_of(p, a0 + k);
-      if (r >= 0)
-        for (int64_t c = l; c < p.D; c += LPT) out[r * p.ldh + c] = x[c];
+      for (int64_t i = c / 16; r >= 0 && i < p.D; i += LPT) out[r * p.ldh + i] = x[i];
     }
     return;
   }
-  for (int64_t c = l * 16; c < p.D; c += LPT * 16) {
-    const int64_t cc = min<int64_t>(c, p.D - 16);
-    const u32x4_t v = load_any(x + cc);
-    for (int k = 0; k < p.topk; ++k) {
-      const int64_t r = row_of(p, a0 + k);
-      if (r >= 0) store_any(out + r * p.ldh + cc, v);
-    }
+  if (c >= p.D) return;
+  const int64_t cc = min<int64_t>(c, p.D - 16);
+  const u32x4_t v = load_any(x + cc);
+  for (int k0 = 0; k0 < p.topk; k0 += kRowsInFlight) {
+    int64_t row[kRowsInFlight];
+#pragma unroll
+    for (int k = 0; k < kRowsInFlight; ++k) row[k] = k0 + k < p.topk ? row_of(p, a0 + k0 + k) : -1;
+#pragma unroll
+    for (int k = 0; k < kRowsInFlight; ++k)
+      if (row[k] >= 0) store_any(out + row[k] * p.ldh + cc, v);
   }
 }
 
 __device__ __forceinline__ float weight_of(const RouteParams& p, int64_t a) {
   return p.w_f32 ? reinterpret_cast<const float*>(p.w)[a] : Elem<uint16_t>::get(reinterpret_cast<const uint16_t*>(p.w)[a]);
 }
-
-constexpr int kRowsInFlight = 8;
 
 template <class T, int LPT, bool W>
 __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) {
@@ -149,21 +149,25 @@ __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) 
   store_any(y + c, Elem<T>::pack(sum));
 }
 
-// DOT: the weights' gradient too; without it h is not read.
+// DOT: the weights' gradient too; without it h is not read. LPT past 64: wavefronts of a block share a token.
 template <class T, int LPT, bool DOT>
-__global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigned token_blocks) {
-  constexpr int VEC = Elem<T>::VEC;
+__global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigned pad_blocks) {
+  constexpr int VEC = Elem<T>::VEC, TPB = 256 / LPT, WPT = LPT / 64;
+  __shared__ float red[DOT && WPT > 1 ? 4 * kRowsInFlight : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (blockIdx.x >= token_blocks) {
+  if (blockIdx.x < pad_blocks) {
     zero_pads(p, reinterpret_cast<uint8_t*>(p.dh), p.D * sizeof(T), p.lddh * sizeof(T),
-              ((int64_t)(blockIdx.x - token_blocks) * 4 + wave) * kPadRows);
+              ((int64_t)blockIdx.x * 4 + wave) * kPadRows);
     return;
   }
-  int64_t t = ((int64_t)blockIdx.x * 4 + wave) * (64 / LPT);
-  if (LPT < 64) t += lane / LPT;
+  int64_t t = (int64_t)(blockIdx.x - pad_blocks) * TPB;
+  if constexpr (WPT > 0)
+    t += wave / WPT;
+  else
+    t += threadIdx.x / LPT;
   const bool live = t < p.tokens;
-  if (LPT == 64 && !live) return;
-  const int l = lane % LPT;
+  if (WPT == 1 && !live) return;
+  const int l = (int)threadIdx.x % LPT;
   const T* dy = reinterpret_cast<const T*>(p.dy) + (live ? t : 0) * p.ldx;
   const T* h = reinterpret_cast<const T*>(p.h);
   T* dh = reinterpret_cast<T*>(p.dh);
@@ -216,10 +220,25 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigne
     if constexpr (!DOT) continue;
 #pragma unroll
     for (int k = 0; k < kRowsInFlight; ++k) {
-      float s = dot[k];
 #pragma unroll
-      for (int o = LPT / 2; o; o >>= 1) s += __shfl_xor(s, o);
-      if (l == 0 && live && k0 + k < p.topk) p.dw[a0 + k0 + k] = s;
+      for (int o = (LPT < 64 ? LPT : 64) / 2; o; o >>= 1) dot[k] += __shfl_xor(dot[k], o);
+    }
+    if constexpr (WPT > 1) {
+      if (k0) __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kRowsInFlight; ++k)
+        if (lane == 0) red[wave * kRowsInFlight + k] = dot[k];
+      __syncthreads();
+      if (l < kRowsInFlight && live && k0 + l < p.topk) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) s += red[(wave + i) * kRowsInFlight + l];
+        p.dw[a0 + k0 + l] = s;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRowsInFlight; ++k)
+        if (l == 0 && live && k0 + k < p.topk) p.dw[a0 + k0 + k] = dot[k];
     }
   }
 }
@@ -231,7 +250,7 @@ namespace {
 // Lanes that hold a row of `chunks` 16-byte chunks: a power of two from 8 to 64.
 int lanes_per_token(int64_t chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64; }
 unsigned blocks_of(int64_t waves) { return (unsigned)((waves + 3) / 4); }
-unsigned pad_blocks(int64_t rows) { return blocks_of((rows + mxf::kPadRows - 1) / mxf::kPadRows); }
+unsigned blocks_of_pads(int64_t rows) { return blocks_of((rows + mxf::kPadRows - 1) / mxf::kPadRows); }
 
 template <class Fn>
 hipError_t with_lanes(int64_t chunks, Fn&& fn) {
@@ -257,24 +276,31 @@ hipError_t launch_combine(const mxf::RouteParams& p, hipStream_t st) {
 
 template <class T, bool DOT>
 hipError_t launch_combine_bwd(const mxf::RouteParams& p, hipStream_t st) {
-  return with_lanes((p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC, [&](auto lanes) {
+  const int64_t chunks = (p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC;
+  const auto go = [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const unsigned tb = blocks_of((p.tokens + 64 / L - 1) / (64 / L));
-    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L, DOT>), dim3(tb + pad_blocks(p.rows)), dim3(256), 0, st, p, tb);
+    const unsigned tb = (unsigned)((p.tokens + 256 / L - 1) / (256 / L));
+    const unsigned pads = blocks_of_pads(p.rows);
+    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L, DOT>), dim3(pads + tb), dim3(256), 0, st, p, pads);
     return hipGetLastError();
-  });
+  };
+  // A block per token for long rows, or few tokens (us with a wavefront per token): 4096 tokens of 8 rows of 7168 BF16 207, 215; of 6
+  // rows of 2048 47, 54; 8 tokens of 6 rows of 2048 5.0, 7.6; but 4096 tokens of 2 rows of 1411 20, 13.
+  if (chunks >= 256 || (chunks > 64 && p.tokens <= 1024)) return go(std::integral_constant<int, 256>());
+  return with_lanes(chunks, go);
 }
 
 }  // namespace
 
 // D, ldx and ldh in bytes.
 hipError_t mxf_launch_dispatch(const mxf::RouteParams& p, hipStream_t st) {
-  return with_lanes((p.D + 15) / 16, [&](auto lanes) {
+  const int64_t chunks = (p.D + 15) / 16, spans = (chunks + 63) / 64;
+  return with_lanes(chunks, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const unsigned tb = blocks_of((p.tokens + 64 / L - 1) / (64 / L));
-    const unsigned n = tb + pad_blocks(p.rows);
-    if (n == 0) return hipSuccess;
-    hipLaunchKernelGGL((mxf::dispatch_kernel<L>), dim3(n), dim3(256), 0, st, p, tb);
+    const unsigned tb = blocks_of(L == 64 ? p.tokens * spans : (p.tokens + 64 / L - 1) / (64 / L));
+    const unsigned pads = blocks_of_pads(p.rows);
+    if (pads + tb == 0) return hipSuccess;
+    hipLaunchKernelGGL((mxf::dispatch_kernel<L>), dim3(pads + tb), dim3(256), 0, st, p, pads, (int)spans);
     return hipGetLastError();
   });
 }
