@@ -1068,6 +1068,12 @@ mxf_status mxfp4_quantize(const mxf_operand_desc* d, const void* x, const int32_
   p.x = x;
   p.q = (uint8_t*)q; p.s = (uint8_t*)s; p.qt = (uint8_t*)qt; p.st = (uint8_t*)st;
   p.offs = offs; p.row_assign = row_assign;
+  if (row_assign) {  // with 2^l the power of two from topk on, m = 2^(30+l) / topk + 1 is over by at most 2^l / topk
+    int l = 0;
+    while ((1 << l) < d->topk) ++l;
+    p.topk_mul = (uint32_t)((1ull << (30 + l)) / (uint32_t)d->topk + 1);
+    p.topk_shift = 30 + l;
+  }
   MXF_HIP(timed("mxfp4_quantize", (hipStream_t)stream, [&] {
             return mxf_launch_mxfp4_quantize(p, f32, (d->flags & MXF_OPERAND_E4M3) != 0, (hipStream_t)stream);
           }), "MXFP4 quantizer launch");

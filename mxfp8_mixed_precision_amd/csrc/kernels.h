@@ -112,6 +112,8 @@ struct Mx4Params {
   const int32_t* offs;
   int E, topk;
   int64_t tokens;
+  uint32_t topk_mul;          // a / topk = a * topk_mul >> topk_shift for a < 2^30
+  int topk_shift;
 };
 
 // Expert products on MXFP4 operands (grouped_mx.hip). Left operand a (E2M1, or E4M3 with a8), right operand b.

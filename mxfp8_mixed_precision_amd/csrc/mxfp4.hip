@@ -17,6 +17,7 @@
 // of codes, 512 bytes of scales), put together in LDS. Bound by HBM.
 #include "chunk.h"
 #include "kernels.h"
+#include "ragged.h"
 
 namespace mxf {
 
@@ -62,6 +63,24 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const GroupScale<tr
   return make_uint2(__builtin_bit_cast(uint32_t, r[0]) | g.nan, __builtin_bit_cast(uint32_t, r[1]) | g.nan);
 }
 
+// The same of packed BF16 pairs, which need no unpacking.
+__device__ __forceinline__ uint32_t codes4(const uint32_t (&v)[4], const GroupScale<false>& g) {
+  uint32_t r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0u, __builtin_bit_cast(bf16x2, v[0]), g.xf, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v[1]), g.xf, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v[2]), g.xf, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v[3]), g.xf, 3);
+  return r | g.nan;
+}
+__device__ __forceinline__ uint2 codes8(const uint32_t (&v)[4], const GroupScale<true>& g) {
+  Scale s;
+  const uint32_t lim = g.byte == 255u ? 0u : (g.byte + 8u) << 7 | 0x60u;  // 448 * 2^e
+  s.lim2 = lim | lim << 16;
+  s.xf = g.xf;
+  s.nanmask = g.nan;
+  s.byte = g.byte;
+  return make_uint2(cvt4(v[0], v[1], s), cvt4(v[2], v[3], s));
+}
+
 // Staging of a tile's codes in LDS: 64-byte rows; 8 rows further another PAD bytes, so that the lanes of a write fall on
 // different banks.
 template <int PAD>
@@ -77,91 +96,142 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(Mx4Params p, unsign
   __shared__ __attribute__((aligned(16))) uint8_t rc[ROW ? NP * SIZER : 16], cc[COL ? NP * SIZEC : 16];
   __shared__ __attribute__((aligned(16))) uint8_t rs[kTile * 4], cs[kTile * 4];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, cg = lane & 15, rl = lane >> 4;
-  const unsigned ct = blockIdx.x % col_tiles, band = blockIdx.x / col_tiles;
+  unsigned ct = blockIdx.x % col_tiles, band = blockIdx.x / col_tiles;
+  if (p.row_assign) {  // a token's rows are far apart: each XCD takes few columns of all rows, which its L2 then holds
+    const unsigned pos = xcd_run(blockIdx.x, gridDim.x);
+    ct = pos / row_tiles;
+    band = pos % row_tiles;
+  }
   const int64_t b = band / row_tiles, rt = band % row_tiles;
   const int64_t r0 = rt * kTile, c0 = (int64_t)ct * kTile;
-  int64_t end = p.rows;
-  if (p.row_assign) end = min<int64_t>(p.offs[p.E], p.rows);
-  if (r0 >= end) return;
   const T* x = reinterpret_cast<const T*>(p.x) + b * p.xs;
   const int64_t n_assign = p.tokens * p.topk, first = r0 + w * 32 + rl * 8;
   const int left = (int)min<int64_t>(p.cols - c0, 1 << 20) - cg * 8;  // columns from the lane's first
 
+  int64_t end = p.rows, from[8];
   bool in[8];
-  const T* src[8];
+  if (p.row_assign) {
+    int32_t a[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = first + i;
-    in[i] = r < end;
-    int64_t from = in[i] ? r : 0;
-    if (p.row_assign) {
-      const int32_t a = in[i] ? p.row_assign[r] : -1;
-      in[i] = a >= 0 && a < n_assign;
-      from = in[i] ? a / p.topk : 0;
+    for (int i = 0; i < 8; ++i) a[i] = p.row_assign[min<int64_t>(first + i, p.rows - 1)];
+    end = min<int64_t>(p.offs[p.E], p.rows);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      in[i] = first + i < end && a[i] >= 0 && a[i] < n_assign;
+      from[i] = in[i] ? (int64_t)(((uint64_t)(uint32_t)a[i] * p.topk_mul) >> p.topk_shift) : 0;  // a / topk
     }
-    src[i] = x + from * p.ldx;
-  }
-  float v[8][8];
-  constexpr int VEC = Elem<T>::VEC, NV = 8 / VEC;
-  if (p.row_assign && p.tokens == 0) {  // pad rows alone
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
   } else {
-    u32x4_t raw[8][NV];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      in[i] = first + i < end;
+      from[i] = in[i] ? first + i : 0;
+    }
+  }
+  if (r0 >= end) return;
+  constexpr int VEC = Elem<T>::VEC, NV = 8 / VEC;
+  u32x4_t raw[8][NV] = {};
+  if (!p.row_assign || p.tokens > 0) {  // (else pad rows alone)
     const int c = (int)c0 + cg * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) raw[i][j] = load_chunk<T, E>(src[i], c + j * VEC, (int)p.cols);
+      for (int j = 0; j < NV; ++j) raw[i][j] = load_chunk<T, E>(x + from[i] * p.ldx, c + j * VEC, (int)p.cols);
+    bool all = left >= 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) all = all && in[i];
+    if (!__all(all)) {  // a ragged edge, or pad rows
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        u32x4_t u = chunk_of<T, E>(raw[i][j], left - j * VEC);
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = in[i] && left > j * VEC ? u[k] : 0u;
-        Elem<T>::unpack(u, &v[i][j * VEC]);
-      }
-  }
-
-  if constexpr (ROW) {
+        for (int j = 0; j < NV; ++j) {
+          raw[i][j] = chunk_of<T, E>(raw[i][j], left - j * VEC);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-      m = max(m, dpp_xor1(m));
-      m = max(m, dpp_xor2(m));
-      const GroupScale<E4M3> g = group_scale<E4M3>(m);
-      const int row = w * 32 + rl * 8 + i;
-      if constexpr (E4M3)
-        *reinterpret_cast<uint2*>(rc + (cg >> 3) * SIZER + staged<PADR>(row) + (cg & 7) * 8) = codes8(v[i], g);
-      else
-        *reinterpret_cast<uint32_t*>(rc + staged<PADR>(row) + cg * 4) = codes4(v[i], g);
-      if ((cg & 3) == 0) rs[row * 4 + (cg >> 2)] = (uint8_t)g.byte;
+          for (int k = 0; k < 4; ++k) raw[i][j][k] = in[i] && left > j * VEC ? raw[i][j][k] : 0u;
+        }
     }
   }
-  if constexpr (COL) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float u[8];
-      uint32_t m = 0;
+
+  // a group's eight of the lane's values with its scale: codes into LDS, the scale byte by one of its lanes
+  const auto put_row = [&](int i, uint32_t amax, const auto& v) {
+    amax = max(amax, dpp_xor1(amax));
+    amax = max(amax, dpp_xor2(amax));
+    const GroupScale<E4M3> g = group_scale<E4M3>(amax);
+    const int row = w * 32 + rl * 8 + i;
+    if constexpr (E4M3)
+      *reinterpret_cast<uint2*>(rc + (cg >> 3) * SIZER + staged<PADR>(row) + (cg & 7) * 8) = codes8(v, g);
+    else
+      *reinterpret_cast<uint32_t*>(rc + staged<PADR>(row) + cg * 4) = codes4(v, g);
+    if ((cg & 3) == 0) rs[row * 4 + (cg >> 2)] = (uint8_t)g.byte;
+  };
+  const auto put_col = [&](int j, uint32_t amax, const auto& v) {
+    const GroupScale<E4M3> g = group_scale<E4M3>(amax);
+    const int col = cg * 8 + j;
+    if constexpr (E4M3)
+      *reinterpret_cast<uint2*>(cc + (w >> 1) * SIZEC + staged<PADC>(col) + (w & 1) * 32 + rl * 8) = codes8(v, g);
+    else
+      *reinterpret_cast<uint32_t*>(cc + staged<PADC>(col) + w * 16 + rl * 4) = codes4(v, g);
+    if (rl == 0) cs[col * 4 + w] = (uint8_t)g.byte;
+  };
+  if constexpr (sizeof(T) == 2) {
+    // magnitudes of BF16 pairs as packed 16-bit integers
+    if constexpr (ROW) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        u[i] = v[i][j];
-        m = max(m, __float_as_uint(u[i]) & 0x7FFFFFFFu);
+        uint32_t v[4], m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = raw[i][0][k];
+          m = pk_max_u16(m, mag2(v[k]));
+        }
+        put_row(i, max(m & 0xFFFFu, m >> 16) << 16, v);
       }
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-      const GroupScale<E4M3> g = group_scale<E4M3>(m);
-      const int col = cg * 8 + j;
-      if constexpr (E4M3)
-        *reinterpret_cast<uint2*>(cc + (w >> 1) * SIZEC + staged<PADC>(col) + (w & 1) * 32 + rl * 8) = codes8(u, g);
-      else
-        *reinterpret_cast<uint32_t*>(cc + staged<PADC>(col) + w * 16 + rl * 4) = codes4(u, g);
-      if (rl == 0) cs[col * 4 + w] = (uint8_t)g.byte;
+    }
+    if constexpr (COL) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // columns 2 k and 2 k + 1
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = pk_max_u16(m, mag2(raw[i][0][k]));
+        m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 16));
+        m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 32));
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = pack_lo(raw[2 * i][0][k], raw[2 * i + 1][0][k]);
+          hi[i] = pack_hi(raw[2 * i][0][k], raw[2 * i + 1][0][k]);
+        }
+        put_col(2 * k, m << 16, lo);
+        put_col(2 * k + 1, m & 0xFFFF0000u, hi);
+      }
+    }
+  } else {
+    if constexpr (ROW) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v[8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          m = max(m, raw[i][k / VEC][k % VEC] & 0x7FFFFFFFu);
+          v[k] = __uint_as_float(raw[i][k / VEC][k % VEC]);
+        }
+        put_row(i, m, v);
+      }
+    }
+    if constexpr (COL) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float v[8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          m = max(m, raw[i][k / VEC][k % VEC] & 0x7FFFFFFFu);
+          v[i] = __uint_as_float(raw[i][k / VEC][k % VEC]);
+        }
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        put_col(k, m, v);
+      }
     }
   }
   __syncthreads();
@@ -195,49 +265,52 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(Mx4Params p, unsign
   }
 }
 
-// Reading back: a block takes 128 rows of one 128-wide piece, 16 lanes a row.
+// Reading back: a block takes 128 rows of one 128-wide piece, a lane 16 bytes of output.
 template <class T, bool E4M3>
 __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(Mx4Params p, unsigned col_tiles, unsigned row_tiles) {
-  constexpr int NP = E4M3 ? 2 : 1, VEC = Elem<T>::VEC;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, cg = lane & 15, rl = lane >> 4;
+  constexpr int NP = E4M3 ? 2 : 1, VEC = Elem<T>::VEC, LPR = 128 / VEC, RPI = 64 / LPR, N = 32 / RPI;  // lanes per row, rows at a time
+  constexpr int BITS = VEC * (E4M3 ? 8 : 4);                                                           // of a lane's codes
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l = lane % LPR, rl = lane / LPR;
   const unsigned ct = blockIdx.x % col_tiles, band = blockIdx.x / col_tiles;
   const int64_t b = band / row_tiles, r0 = (int64_t)(band % row_tiles) * kTile + w * 32 + rl;
-  const int64_t plane = (b * col_tiles + ct) * p.rows, c0 = (int64_t)ct * kTile + cg * 8;
-  const int64_t panel = NP * plane + (E4M3 ? (cg >> 3) * p.rows : 0);
-  const int n = (int)min<int64_t>(p.cols - c0, 8);
-  uint32_t k[8][2];
-  float sc[8];
+  const int64_t plane = (b * col_tiles + ct) * p.rows, c0 = (int64_t)ct * kTile + l * VEC;
+  const int64_t panel = NP * plane + (E4M3 ? (l * VEC >> 6) * p.rows : 0);
+  const int n = (int)min<int64_t>(p.cols - c0, VEC), at = l * BITS / 8 % 64;
+  uint32_t k[N][2];
+  uint32_t sc[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = min<int64_t>(r0 + 4 * i, p.rows - 1);
-    const uint8_t* q = p.q + (panel + r) * 64 + (E4M3 ? (cg & 7) * 8 : cg * 4);
-    k[i][0] = *reinterpret_cast<const uint32_t*>(q);
-    k[i][1] = E4M3 ? *reinterpret_cast<const uint32_t*>(q + 4) : 0u;
-    sc[i] = ckpt_scale(p.s[(plane + r) * 4 + (cg >> 2)]);
+  for (int i = 0; i < N; ++i) {
+    const int64_t r = min<int64_t>(r0 + RPI * i, p.rows - 1);
+    const uint8_t* q = p.q + (panel + r) * 64 + at;
+    k[i][1] = 0;
+    if constexpr (BITS == 16)
+      k[i][0] = *reinterpret_cast<const uint16_t*>(q);
+    else
+      k[i][0] = *reinterpret_cast<const uint32_t*>(q);
+    if constexpr (BITS == 64) k[i][1] = *reinterpret_cast<const uint32_t*>(q + 4);
+    sc[i] = p.s[(plane + r) * 4 + (l * VEC >> 5)];
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 4 * i;
-    float f[8];
+  for (int i = 0; i < N; ++i) {
+    const int64_t r = r0 + RPI * i;
+    const float scale = ckpt_scale(sc[i]);
+    float f[VEC];
     if constexpr (E4M3) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = ckpt_value(k[i], j, sc[i]);
+      for (int j = 0; j < VEC; ++j) f[j] = ckpt_value(k[i], j, scale);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < VEC / 2; ++j) {
         const f32x2 u = j == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(k[i][0], 1.0f, 0)
                         : j == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(k[i][0], 1.0f, 1)
                         : j == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(k[i][0], 1.0f, 2)
                                  : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(k[i][0], 1.0f, 3);
-        f[2 * j] = u[0] * sc[i];
-        f[2 * j + 1] = u[1] * sc[i];
+        f[2 * j] = u[0] * scale;
+        f[2 * j + 1] = u[1] * scale;
       }
     }
     T* o = reinterpret_cast<T*>(p.out) + (b * p.rows + r) * p.cols + c0;
-    if (r < p.rows) {
-#pragma unroll
-      for (int j = 0; j < 8 / VEC; ++j) store_chunk<T, INSIDE>(o + j * VEC, f + j * VEC, n - j * VEC);
-    }
+    if (r < p.rows) store_chunk<T, INSIDE>(o, f, n);
   }
 }
 
