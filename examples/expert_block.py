@@ -4,8 +4,8 @@
 
 y = x + sum_k p[t, k] W2[e] swiglu(W13[e] norm(x)[t]),  e = choice[t, k]
 
-Layer norm -> routing plan and permute (segments not padded) -> ragged product -> SwiGLU -> ragged product ->
-weighted sum. What the backward needs is kept as MXFP8: the normalised rows, the first product's input and
+Layer norm -> routing plan and dispatch (segments not padded) -> ragged product -> SwiGLU -> ragged product ->
+combine. What the backward needs is kept as MXFP8: the normalised rows, the first product's input and
 the gate and up rows (1.03 bytes per element instead of 2); the second product's input is computed again.
 The router is an input here: its choices and weights are given.
 """
@@ -35,32 +35,28 @@ class ExpertBlock:
         else:
             n = mx.layer_norm_fwd(x, self.norm_w, self.norm_b, stats=False)
         plan = mx.route_plan(choice, E, 1, T * k)  # pad_multiple 1: every row is a token's
-        offs, rows = plan["offs"], plan["row_assign"].long()
-        xp = torch.empty((T * k, D), dtype=torch.bfloat16, device=x.device)
-        mx.mxf_dispatch_permute(n, T, k, D, E, offs, plan["row_assign"], T * k, xp)
+        offs = plan["offs"]
+        xp = mx.dispatch_fwd(n, plan)
         gu = mx.grouped_gemm_fwd(xp, self.w13, offs)
         h, qh, sh = mx.swiglu_ckpt_fwd(gu)
         yp = mx.grouped_gemm_fwd(h, self.w2, offs)
-        picked = yp[plan["assign_row"].long()].view(T, k, D).float()
-        y = (x.float() + (picked * weight[:, :, None]).sum(1)).bfloat16()
+        y = mx.combine_fwd(yp, weight, plan, x)
         if not keep:
             return y
         qx, sx, _, _ = mx.quantize(xp, mx.ROW)
-        return y, dict(norm=(qn, sn, rstd), x=(qx, sx), h=(qh, sh), offs=offs, rows=rows,
-                       back=plan["assign_row"].long(), weight=weight)
+        return y, dict(norm=(qn, sn, rstd), x=(qx, sx), h=(qh, sh), plan=plan, weight=weight)
 
     def backward(self, dy, kept):
         """dy [T, D] BF16. Returns dx (BF16) and the FP32 gradients of norm_w, norm_b, w13 and w2."""
-        T, D = dy.shape
-        k = kept["weight"].shape[1]
-        offs, rows = kept["offs"], kept["rows"]
-        dyp = (dy[rows // k].float() * kept["weight"].reshape(-1)[rows][:, None]).bfloat16()
+        plan = kept["plan"]
+        offs = plan["offs"]
+        dyp, _ = mx.combine_bwd(dy, None, kept["weight"], plan)  # (the weights are given: no gradient of theirs)
         dh = mx.grouped_gemm_dgrad(dyp, self.w2, offs)
         dgu, h = mx.swiglu_ckpt_bwd(dh, *kept["h"])
         dw2 = mx.grouped_gemm_wgrad(dyp, h, offs, out_dtype=torch.float32)
         dxp = mx.grouped_gemm_dgrad(dgu, self.w13, offs)
         dw13 = mx.grouped_gemm_wgrad(dgu, kept["x"], offs, out_dtype=torch.float32)
-        dn = dxp[kept["back"]].view(T, k, D).float().sum(1).bfloat16()
+        dn = mx.dispatch_bwd(dxp, plan, dy.shape[0])
         dx, dnw, dnb = mx.layer_norm_ckpt_bwd(dn, *kept["norm"], self.norm_w)
         return (dx.float() + dy.float()).bfloat16(), dnw, dnb, dw13, dw2
 
