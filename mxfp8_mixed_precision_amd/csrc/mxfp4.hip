@@ -14,7 +14,13 @@
 //
 // A block takes a tile of 128 x 128: a quarter of a wavefront reads 8 rows of it, 8 columns a lane, so a row group is
 // four lanes, a column group the same column of four quarters, and all four outputs of the tile are contiguous runs (8 KB
-// of codes, 512 bytes of scales), put together in LDS. Bound by HBM.
+// of codes, 512 bytes of scales), put together in LDS. A tile's amax takes four exchanges of packed pairs for the columns and two for
+// the rows. BF16 values go through in pairs (v_cvt_scalef32_pk_fp4_bf16, 16-bit magnitudes), FP32 ones one by one.
+//
+// FP32 is bound by HBM: 16 weights of 2816 x 2048, rows 71 us (5.7 TB/s), and as BF16 read back 34 (6.6 TB/s). BF16 in both
+// directions is not: 24576 x 2048 28.4, rows alone 23.9 (6.3 TB/s). Gathered rows (a plan's, topk 6) would be read topk times
+// from memory where neighbouring tiles of a row land on different XCDs; each XCD takes a run of row tiles, whose rows are in its L2 for
+// all their columns: 25.0 us for 24576 x 2048 in both directions, 18 MB read.
 #include "chunk.h"
 #include "kernels.h"
 #include "ragged.h"
