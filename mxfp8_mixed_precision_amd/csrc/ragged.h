@@ -68,7 +68,7 @@ __device__ __forceinline__ bool ragged_ok(const int32_t* offs, int E, int64_t M)
   return !__any(bad);
 }
 
-// The place-th segment in falling order of rows (ties in index order); in index order past 64 experts. Valid offsets.
+// The place-th segment in falling order of rows (to 64 rows; then in any order); in index order past 64 experts. Valid offsets.
 struct Segment {
   int e, lo, hi;
 };
@@ -79,11 +79,9 @@ __device__ __forceinline__ Segment by_length(const int32_t* offs, int E, int pla
   }
   const int lane = threadIdx.x & 63;
   const int lo = lane < E ? offs[lane] : 0, hi = lane < E ? offs[lane + 1] : -1, n = hi - lo;
+  const int key = n < 0 ? -1 : (n >> 6) << 6 | (63 - lane);  // (unique; experts of nearly equal lengths come in any order)
   int rank = 0;
-  for (int j = 0; j < E; ++j) {
-    const int nj = __builtin_amdgcn_readlane(n, j);
-    rank += nj > n || (nj == n && j < lane);
-  }
+  for (int j = 0; j < E; ++j) rank += __builtin_amdgcn_readlane(key, j) > key;
   const int e = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(lane < E && rank == place)) - 1);
   return {e, __builtin_amdgcn_readlane(lo, e), __builtin_amdgcn_readlane(hi, e)};
 }
