@@ -34,6 +34,8 @@ def _plan(plan, device, rows=None):
 
 def _topk(assign_row, tokens):
     n = assign_row.numel()
+    if tokens < 0:
+        _bad(f"{tokens} tokens")
     if tokens == 0:
         if n:
             _bad(f"plan: {n} assignments of no tokens")
@@ -54,7 +56,8 @@ def _float_flag(t, name):
 
 @_on_stream
 def dispatch_fwd(x, plan):
-    """xe [rows, D]: row r is token row_assign[r] // topk of x [tokens, D], zeros for a pad row. Any element type."""
+    """xe [rows, D]: row r is token row_assign[r] // topk of x [tokens, D], zeros for a pad row. Any type with
+    elements of 1, 2, 4 or 8 bytes."""
     torch = _t()
     tokens, D, ld = _rows(x, "x")
     dev = x.device

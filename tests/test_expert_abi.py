@@ -149,7 +149,7 @@ def test_tensor_calls_refuse_what_does_not_fit():
         (mx.dispatch_fwd, (x, but(row_assign=plan["row_assign"].long()))), (mx.dispatch_fwd, (x, but(assign_row=plan["assign_row"][::2]))),
         (mx.dispatch_fwd, (x[:0], plan)), (mx.dispatch_fwd, (x, but(assign_row=plan["assign_row"][:3]))),
         (mx.dispatch_bwd, (h, plan, 3)), (mx.dispatch_bwd, (h[:9], plan, 4)), (mx.dispatch_bwd, (h.half(), plan, 4)),
-        (mx.dispatch_bwd, (h, plan, 16)),
+        (mx.dispatch_bwd, (h, plan, 16)), (mx.dispatch_bwd, (h, plan, -4)),
         (mx.combine_fwd, (h, None, plan)), (mx.combine_fwd, (h, w[:3], plan)), (mx.combine_fwd, (h, w.half(), plan)),
         (mx.combine_fwd, (h, w[:, :1], plan)), (mx.combine_fwd, (h, w, plan, x.float())), (mx.combine_fwd, (h, w, plan, x[:3])),
         (mx.combine_bwd, (dy, h[:9], w, plan)), (mx.combine_bwd, (dy, h.float(), w, plan)), (mx.combine_bwd, (dy, h, None, plan)),
