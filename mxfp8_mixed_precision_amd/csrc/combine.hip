@@ -13,8 +13,9 @@
 // of row_assign to a wavefront, and in dispatch and the gradient these come first.
 //
 // Bound by HBM (copy: 6.1 TB/s; BF16): dispatch of 4096 tokens to 24576 rows of 2048 and the padding 20.6 us (127 MB, 5.9 TB/s;
-// by whole tokens 25.7); combine back 18.2 (119 MB, 6.1 TB/s); gradient of 4096 tokens, 32768 rows of 7168 and the padding 206
-// (1057 MB, 5.0 TB/s; 64 lanes per token 220: a lane then holds a row's chunks one after the other). Combine of 8 tokens: 3.9.
+// by whole tokens 25.7); combine back 18.2 (119 MB, 6.1 TB/s); gradient of 4096 tokens, 32768 rows of 7168 and the padding 191
+// (1057 MB, 5.5 TB/s; h through the caches 206, with 64 lanes per token, which hold a row's chunks one after the other, 220).
+// Combine of 8 tokens: 3.9.
 //
 // A row's last chunk is taken from its end backwards, over elements that its neighbour has too: both store the same
 // values (the dot products skip them), so any width and alignment goes without a branch. Rows shorter than a chunk
@@ -37,6 +38,9 @@ __device__ __forceinline__ u32x4_t load_any(const void* p) {
   u32x4_t v;
   __builtin_memcpy(&v, p, 16);
   return v;
+}
+__device__ __forceinline__ u32x4_t load_once(const void* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
 }
 __device__ __forceinline__ void store_any(void* p, u32x4_t v) {
   __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
@@ -63,7 +67,7 @@ __device__ __forceinline__ void zero_pads(const RouteParams& p, uint8_t* out, in
   }
 }
 
-// LPT lanes per token; with 64 a wavefront takes one span of 64 chunks of it.
+// LPT lanes per token; with 64 a wavefront takes one span of 64 chunks of it. (combine, ONCE: h is read past the caches.)
 template <int LPT>
 __global__ __launch_bounds__(256) void dispatch_kernel(RouteParams p, unsigned pad_blocks, int spans) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -101,7 +105,7 @@ __device__ __forceinline__ float weight_of(const RouteParams& p, int64_t a) {
   return p.w_f32 ? reinterpret_cast<const float*>(p.w)[a] : Elem<uint16_t>::get(reinterpret_cast<const uint16_t*>(p.w)[a]);
 }
 
-template <class T, int LPT, bool W>
+template <class T, int LPT, bool W, bool ONCE>
 __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) {
   constexpr int VEC = Elem<T>::VEC;
   const int lane = threadIdx.x & 63;
@@ -140,7 +144,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) 
       in[k] = k0 + k < p.topk && r >= 0;
       w[k] = W ? weight_of(p, a) : 1.0f;
       v[k] = (u32x4_t){0, 0, 0, 0};
-      if (in[k]) v[k] = load_any(h + r * p.ldh + c);
+      if (in[k]) v[k] = ONCE ? load_once(h + r * p.ldh + c) : load_any(h + r * p.ldh + c);
     }
 #pragma unroll
     for (int k = 0; k < kRowsInFlight; ++k) {
@@ -154,8 +158,9 @@ __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) 
   store_any(y + c, Elem<T>::pack(sum));
 }
 
-// DOT: the weights' gradient too; without it h is not read. LPT past 64: wavefronts of a block share a token.
-template <class T, int LPT, bool DOT>
+// DOT: the weights' gradient too; without it h is not read. LPT past 64: wavefronts of a block share a token. ONCE: h is read past the
+// caches.
+template <class T, int LPT, bool DOT, bool ONCE>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigned pad_blocks) {
   constexpr int VEC = Elem<T>::VEC, TPB = 256 / LPT, WPT = LPT / 64;
   __shared__ float red[DOT && WPT > 1 ? 4 * kRowsInFlight : 1];
@@ -205,7 +210,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigne
         u32x4_t v[kRowsInFlight];
 #pragma unroll
         for (int k = 0; k < kRowsInFlight; ++k)
-          if (DOT && row[k] >= 0) v[k] = load_any(h + row[k] * p.ldh + c);
+          if (DOT && row[k] >= 0) v[k] = ONCE ? load_once(h + row[k] * p.ldh + c) : load_any(h + row[k] * p.ldh + c);
         float g[VEC];
         Elem<T>::unpack(gv, g);
 #pragma unroll
@@ -257,6 +262,12 @@ int lanes_per_token(int64_t chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16
 unsigned blocks_of(int64_t waves) { return (unsigned)((waves + 3) / 4); }
 unsigned blocks_of_pads(int64_t rows) { return blocks_of((rows + mxf::kPadRows - 1) / mxf::kPadRows); }
 
+// Whether h (`copies` 2: and dh) fills most of the 256 MB last-level cache, so that none of it is still there: it is read past the caches
+// then, where its rows are whole 128-byte lines (a line that two instructions share would come twice).
+bool read_once(const mxf::RouteParams& p, int64_t size, int64_t copies) {
+  return p.ldh * size % 128 == 0 && ((uintptr_t)p.h & 127) == 0 && copies * p.tokens * p.topk * p.D * size >= ((int64_t)192 << 20);
+}
+
 template <class Fn>
 hipError_t with_lanes(int64_t chunks, Fn&& fn) {
   switch (lanes_per_token(chunks)) {
@@ -267,26 +278,26 @@ hipError_t with_lanes(int64_t chunks, Fn&& fn) {
   }
 }
 
-template <class T, bool W>
+template <class T, bool W, bool ONCE>
 hipError_t launch_combine(const mxf::RouteParams& p, hipStream_t st) {
   const int64_t chunks = (p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC;
   const int64_t spans = (chunks + 63) / 64;
   return with_lanes(chunks, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
     const int64_t waves = L == 64 ? p.tokens * spans : (p.tokens + 64 / L - 1) / (64 / L);
-    hipLaunchKernelGGL((mxf::combine_kernel<T, L, W>), dim3(blocks_of(waves)), dim3(256), 0, st, p, (int)spans);
+    hipLaunchKernelGGL((mxf::combine_kernel<T, L, W, ONCE>), dim3(blocks_of(waves)), dim3(256), 0, st, p, (int)spans);
     return hipGetLastError();
   });
 }
 
-template <class T, bool DOT>
+template <class T, bool DOT, bool ONCE>
 hipError_t launch_combine_bwd(const mxf::RouteParams& p, hipStream_t st) {
   const int64_t chunks = (p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC;
   const auto go = [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
     const unsigned tb = (unsigned)((p.tokens + 256 / L - 1) / (256 / L));
     const unsigned pads = blocks_of_pads(p.rows);
-    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L, DOT>), dim3(pads + tb), dim3(256), 0, st, p, pads);
+    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L, DOT, ONCE>), dim3(pads + tb), dim3(256), 0, st, p, pads);
     return hipGetLastError();
   };
   // A block per token for long rows, or few tokens (us with a wavefront per token): 4096 tokens of 8 rows of 7168 BF16 207, 215; of 6
@@ -311,11 +322,19 @@ hipError_t mxf_launch_dispatch(const mxf::RouteParams& p, hipStream_t st) {
 }
 
 hipError_t mxf_launch_combine(const mxf::RouteParams& p, bool f32, hipStream_t st) {
-  if (p.w) return f32 ? launch_combine<float, true>(p, st) : launch_combine<uint16_t, true>(p, st);
-  return f32 ? launch_combine<float, false>(p, st) : launch_combine<uint16_t, false>(p, st);
+  // (us, through the caches): 4096 tokens of 8 rows of 7168 BF16 89, 96; of 6 rows of 2048 FP32 40, 43.5; but 8192 tokens of 4
+  // rows of 1411 BF16 21.5, 20
+  if (p.w && read_once(p, f32 ? 4 : 2, 1))
+    return f32 ? launch_combine<float, true, true>(p, st) : launch_combine<uint16_t, true, true>(p, st);
+  if (p.w) return f32 ? launch_combine<float, true, false>(p, st) : launch_combine<uint16_t, true, false>(p, st);
+  return f32 ? launch_combine<float, false, false>(p, st) : launch_combine<uint16_t, false, false>(p, st);
 }
 
 hipError_t mxf_launch_combine_bwd(const mxf::RouteParams& p, bool f32, hipStream_t st) {
-  if (p.dw) return f32 ? launch_combine_bwd<float, true>(p, st) : launch_combine_bwd<uint16_t, true>(p, st);
-  return f32 ? launch_combine_bwd<float, false>(p, st) : launch_combine_bwd<uint16_t, false>(p, st);
+  if (!p.dw) return f32 ? launch_combine_bwd<float, false, false>(p, st) : launch_combine_bwd<uint16_t, false, false>(p, st);
+  // (us, through the caches): 4096 tokens of 8 rows of 7168 BF16 191, 206; of 2 rows of 4096 FP32 62, 71; of 6 rows of 2048 BF16
+  // 46, 49; but 8192 tokens of 8 rows of 512 BF16, 134 MB of which a part is still there, 31.5, 26.3; 512 tokens of 8 rows of 5120 20, 18.
+  if (read_once(p, f32 ? 4 : 2, 2))
+    return f32 ? launch_combine_bwd<float, true, true>(p, st) : launch_combine_bwd<uint16_t, true, true>(p, st);
+  return f32 ? launch_combine_bwd<float, true, false>(p, st) : launch_combine_bwd<uint16_t, true, false>(p, st);
 }

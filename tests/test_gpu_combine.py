@@ -99,6 +99,12 @@ def test_against_float64(T, topk, E, D, pad, drop, ld, off, t):
         assert torch.equal(again[0][:end], dh[:end]) and torch.equal(again[1], dw)
 
 
+# h, or h and dh, larger than the last-level cache
+@pytest.mark.parametrize("T,topk,D,t", [(4096, 8, 4096, BF), (4096, 6, 2048, F32), (8192, 4, 2048, BF)])
+def test_rows_past_the_cache(T, topk, D, t):
+    test_against_float64(T, topk, 16, D, 128, 0.01, 0, 0, t)
+
+
 @pytest.mark.parametrize("dtype", [torch.uint8, torch.int8, torch.float16, torch.int32, torch.int64, torch.float64])
 @pytest.mark.parametrize("D", [1, 3, 16, 65, 1000])
 def test_dispatch_moves_any_type(dtype, D):
