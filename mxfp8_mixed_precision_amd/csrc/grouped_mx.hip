@@ -337,8 +337,8 @@ __global__ __launch_bounds__(256, OCC) void grouped_mx_rows_kernel(GroupedMxPara
 // each of 16 stages, or four to each of 8 where a tile has fewer than 16.
 //
 // 24576 x 2816 x 2048, 16 experts, 85 us (3.3 PFLOP/s; tiles one by one 90, compute 40 at the instructions' rate): a tile is 16
-// stages, and the chip stores 138 MB at the same time. 16384 x 4096 x 7168, 8 experts, 224-240 us (4.0-4.3 PFLOP/s), 8192^3 235 (4.7): matrix
-// cores busy 58% of the cycles at 1.73 GHz, to which the power limit lowers the clock (2.4 without load).
+// stages, and the chip stores 138 MB at the same time. 16384 x 4096 x 7168, 8 experts, 224-240 us (4.0-4.3 PFLOP/s), 8192^3 235 (4.7):
+// matrix cores busy 58% of the cycles at 1.73 GHz, to which the power limit lowers the clock (2.4 without load).
 constexpr int kStreamTiles = 1024;  // of a block: its list is in LDS
 
 struct StreamTile {
