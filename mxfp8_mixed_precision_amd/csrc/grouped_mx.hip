@@ -6,7 +6,9 @@
 // The input gradient is a forward product of dy with the column operand of w. The right operand is E2M1, the left E2M1 or
 // E4M3. v_mfma_scale_f32_32x32x64_f8f6f4 multiplies the codes, applies both scales and adds to FP32. Within eight
 // neighbouring products it keeps 13 places below the largest's exponent, which holds all of E2M1 x E2M1 (2.8e-7 over 16384
-// random terms) but not of E4M3 x E2M1 (4e-5).
+// random terms) but not of E4M3 x E2M1. So E4M3 codes go in two parts, magnitudes from 2 on and those below, zeros in the place of
+// the others: products of the first are multiples of 2^-3 (codes of 2^-2, E2M1 of 2^-1) with exponents up to 10, of the second
+// multiples of 2^-10 with exponents up to 2, and both fit. That doubles the instructions, which E4M3 halves the rate of already.
 #include <type_traits>
 
 #include "chunk.h"
@@ -19,6 +21,12 @@ namespace mxf {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// The E4M3 codes of magnitudes from 2 on (bit 6 of a byte), zeros in the place of the others.
+__device__ __forceinline__ int large_codes(int v) {
+  // (selectors 8 to 11 fill a byte with bit 15 or 31 of the second or first word)
+  return v & (int)__builtin_amdgcn_perm((uint32_t)v << 1, (uint32_t)v << 9, 0x0B090A08u);
+}
+
 // Operand layout in registers: for 64 of the contraction lane l = r + 32 g (r < 32, g < 2) holds row r's E2M1 codes
 // [32 g, 32 g + 32), 16 bytes, and the scale of that group; of E4M3 codes [16 g, 16 g + 16) and [32 + 16 g, 48 + 16 g), and
 // the scale of group g all the same.
@@ -29,8 +37,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // Rows that do not exist load as zeros (bounded loads), the contraction is padded by the layout.
 //
 // Measured (us; instructions alone at 7.2 PFLOP/s, E4M3 x E2M1 4.6): weight gradient of 24576 x 2816 x 2048, 16 experts, into FP32 114
-// (compute 40, the 369 MB of stores 61, one after the other in a tile; into BF16 94); forward of 48 E4M3 rows of 16 experts of
-// 2816 x 2048 9.6 (latency of a tile's 16 stages; 34 MB read); 24576 x 2816 x 2048 with E4M3 rows 130.
+// (compute 40, the 369 MB of stores 61, one after the other in a tile; into BF16 94); forward of 24576 x 2816 x 2048 with E4M3
+// rows 205 (instructions 123; with one product for all codes, right to 4e-5 alone, 130).
 template <int BM, int BN, bool A8, int S_>
 struct MxTile {
   static constexpr int S = S_;
@@ -161,15 +169,33 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
 
   f32x16 acc[FM][FN];
   // the operands swap places: a lane holds one output row and, in runs of four accumulators, four neighbouring columns
-  auto multiply = [&](int m, auto ks_) {
-    constexpr int ks = decltype(ks_)::value;
-    const int i = m / FN, j = m % FN;
-    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[ks][j], fa[ks][i], acc[i][j], 4, A8 ? 0 : 4, 2 * ks, (int)sb[j],
-                                                                2 * ks, (int)sa[i]);
+  // E4M3: per fragment of A all products with its large codes, beside which the small ones are made, then those with the small ones,
+  // beside which the next fragment's large ones are (always after the product, which would wait for them). LIVE: fragments
+  // that have rows.
+  constexpr int PARTS = A8 ? 2 : 1;
+  i32x8 part[2];
+  auto multiply = [&](auto m_, auto ks_, auto live_) {
+    constexpr int m = decltype(m_)::value, ks = decltype(ks_)::value, LIVE = decltype(live_)::value;
+    constexpr int i = m / (PARTS * FN), h = m / FN % PARTS, j = m % FN;
+    if constexpr (i < LIVE) {
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[ks][j], A8 ? part[h] : fa[ks][i], acc[i][j], 4, A8 ? 0 : 4, 2 * ks,
+                                                                  (int)sb[j], 2 * ks, (int)sa[i]);
+      if constexpr (A8) {
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int n = (i + 1) % LIVE;
+#pragma unroll
+        for (int q = 8 * j / FN; q < 8 * (j + 1) / FN; ++q) {
+          if (h)
+            part[0][q] = large_codes(fa[n ? ks : 1 - ks][n][q]);
+          else
+            part[1][q] = fa[ks][i][q] ^ part[0][q];
+        }
+      }
+    }
   };
   using K0 = std::integral_constant<int, 0>;
   using K1 = std::integral_constant<int, 1>;
-  constexpr int NM = FM * FN;
+  constexpr int NM = PARTS * FM * FN;
   if (KT == 0) none();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) {
@@ -189,20 +215,25 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
   uint32_t slot = 0;
   auto after = [](uint32_t st) { return st == (S - 1) * T::STAGE ? 0u : st + (uint32_t)T::STAGE; };
   if (KT > 0) {
-      wait_vmcnt<(S - 2) * T::L + LH>();
-      __syncthreads();
+    wait_vmcnt<(S - 2) * T::L + LH>();
+    __syncthreads();
 #pragma unroll
-      for (int r = 0; r < FM + FN; ++r) read_scale(r, 0);
+    for (int r = 0; r < FM + FN; ++r) read_scale(r, 0);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) read(r, 0, 0);
-      take_scales();
-      uint32_t last = (S - 1) * T::STAGE;
+    for (int r = 0; r < NR; ++r) read(r, 0, 0);
+    take_scales();
+    if constexpr (A8) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) part[0][q] = large_codes(fa[0][0][q]);
+    }
+    uint32_t last = (S - 1) * T::STAGE;
+    const auto stages = [&](auto live) {
 #pragma unroll 1
       for (int kt = 0; kt < KT; ++kt) {
         // first half, beside the reads of the second and the rest of the loads of stage kt + S - 1
         each<NM>([&](auto m_) {
           constexpr int m = decltype(m_)::value, l0 = LH + m * (T::L - LH) / NM, l1 = LH + (m + 1) * (T::L - LH) / NM;
-          multiply(m, K0());
+          multiply(m_, K0(), live);
 #pragma unroll
           for (int r = m * NR * 2 / NM; r < (m + 1) * NR * 2 / NM && r < NR; ++r) read(r, 1, slot);
           each<l1 - l0>([&](auto i) { load(std::integral_constant<int, l0 + decltype(i)::value>(), lds0 + last); });
@@ -216,7 +247,7 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
         // second half, beside the reads of the next stage's first and the first loads of stage kt + S
         each<NM>([&](auto m_) {
           constexpr int m = decltype(m_)::value, l0 = m * LH / NM, l1 = (m + 1) * LH / NM, NRS = NR + FM + FN;
-          multiply(m, K1());
+          multiply(m_, K1(), live);
 #pragma unroll
           for (int r = m * NRS * 2 / NM; r < (m + 1) * NRS * 2 / NM && r < NRS; ++r) {
             if (r < FM + FN)
@@ -231,6 +262,20 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
         last = slot;
         slot = next;
       }
+    };
+    using F = std::integral_constant<int, FM>;
+    if constexpr (A8 && FN == 2) {  // (a wavefront's rows may end in its first fragment, or before; all pass the same barriers)
+      static_assert(FM == 2);
+      const int live = (mr - wm * (BM / 2) + 31) >> 5;
+      if (live <= 0)
+        stages(std::integral_constant<int, 0>());
+      else if (live < FM)
+        stages(std::integral_constant<int, 1>());
+      else
+        stages(F());
+    } else {
+      stages(F());
+    }
   }
   wait_vmcnt<0>();  // no load may still target LDS
   __syncthreads();  // the slots become the epilogue's staging
@@ -713,16 +758,22 @@ __device__ __forceinline__ void few_rows(float* red, const MxOperand& a, const M
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         if (i && !both) continue;
-        i32x8 va = {};
+        i32x8 codes = {};
 #pragma unroll
-        for (int q = 0; q < (A8 ? 8 : 4); ++q) va[q] = (int)fa[u][i][q / 4][q % 4];
+        for (int q = 0; q < (A8 ? 8 : 4); ++q) codes[q] = (int)fa[u][i][q / 4][q % 4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          i32x8 vb = {};
+        for (int h = 0; h < (A8 ? 2 : 1); ++h) {
+          i32x8 va = codes;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) vb[q] = (int)fb[u][j][q];
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc[i][j], A8 ? 0 : 4, 4, 0, (int)(sa[u][i] >> (8 * g)),
-                                                                       0, (int)(sb[u][j] >> (8 * g)));
+          for (int q = 0; A8 && q < 8; ++q) va[q] = h ? codes[q] ^ large_codes(codes[q]) : large_codes(codes[q]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            i32x8 vb = {};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) vb[q] = (int)fb[u][j][q];
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc[i][j], A8 ? 0 : 4, 4, 0, (int)(sa[u][i] >> (8 * g)),
+                                                                         0, (int)(sb[u][j] >> (8 * g)));
+          }
         }
       }
     }
@@ -792,8 +843,11 @@ hipError_t launch(bool wgrad, const GroupedMxParams& p, int ncu, hipStream_t st)
   // share it (us, in tiles): one row 4096 x 4096 4.0, 10.1; 4 experts of 4096 x 4096, 8 rows each 8.4, 10.6; one expert of 1024
   // x 8192, 200 rows 7.3, 17.1; 32 experts of 300 x 7168, 3 rows each 10.8, 15.5. With more blocks a strip's own cost weighs more: 16
   // experts of 2816 x 2048, 32 rows each 13.8, 12.2; 256 experts, 1 row each 212, 161.
-  const int64_t fct = (p.N + FC - 1) / FC, frt = p.M / FR + met;
-  if (!wgrad && frt * ((p.N + 127) / 128) <= 3 * ncu / 4) {
+  // E4M3 rows, whose instructions cost twice as much, share a long contraction out further, and with few rows to an expert for any
+  // number of strips (us, in tiles): 16 experts of 2816 x 2048, 3 rows each 12.6, 14.4, 32 rows each 18.0, 14.6; 64 experts, 3 rows
+  // each 45.8, 67, 16 rows each 68.7, 68.4; 64 experts of 2048 x 1408, 4 rows each 28.5, 32.2; but of 1024 x 512 11.6, 10.5.
+  const int64_t fct = (p.N + FC - 1) / FC, frt = p.M / FR + met, fs = frt * ((p.N + 127) / 128);
+  if (!wgrad && (fs <= 3 * ncu / 4 || (A8 && p.K > 1024 && (fs <= 7 * ncu / 4 || p.M <= 8 * met) && frt * fct < (1 << 23)))) {
     hipLaunchKernelGGL(grouped_mx_few_rows_kernel<A8>, dim3((unsigned)(frt ? frt * fct : 1)), dim3(64 * FW), 0, st, p, (int)fct);
     return hipGetLastError();
   }
