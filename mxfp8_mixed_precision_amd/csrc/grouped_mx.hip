@@ -400,10 +400,10 @@ __device__ __forceinline__ void swap_eights(u32x4_t& x, u32x4_t& y) {
   }
 }
 
-__device__ __forceinline__ void store16_bounded(u32x4_t v, i32x4 rsrc, uint32_t voff, uint32_t soff) {
+__device__ __forceinline__ void store16_bounded(u32x4_t v, i32x4 rsrc, uint32_t voff) {
   const __amdgpu_buffer_rsrc_t r =
       __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)(uint32_t)rsrc[1] << 32 | (uint32_t)rsrc[0]), 0, rsrc[2], 0x00020000);
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), r, voff, soff, 2);  // (non-temporal)
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), r, voff, 0, 2);  // (non-temporal)
 }
 
 template <int PRE>
@@ -502,13 +502,13 @@ __device__ __forceinline__ void stream_tiles(const GroupedMxParams& p, uint8_t* 
 #pragma unroll
   for (int m = 0; m < NM; ++m) done[m][0] = done[m][1] = (u32x4_t){0, 0, 0, 0};
   i32x4 ro = {0, 0, 0, 0x00020000};  // (nothing to store yet)
-  uint32_t vo = 0;
+  uint32_t vo[2] = {kNoElement, kNoElement};  // columns col and 64 + col of the lane's first row
   const int col = wn * 128 + 8 * g + 16 * ((lane >> 4) & 1) + 32 * ((lane >> 3) & 1);
-  int left = 0;  // columns from the lane's first to the tile's end
   const uint32_t eight_rows = (uint32_t)p.ldc * 16;
   auto store = [&](auto k_) {
-    constexpr int k = decltype(k_)::value, m = k / 2, h = k % 2, c = m % FN / 2 * 64;
-    store16_bounded(done[m][h], ro, c < left ? vo + c * 2 : kNoElement, (m / FN * 4 + h * 2 + m % 2) * eight_rows);
+    constexpr int k = decltype(k_)::value, m = k / 2, h = k % 2;
+    // (rows past the tile's are found by the whole offset: an instruction's scalar offset need not be part of the bounds check)
+    store16_bounded(done[m][h], ro, vo[m % FN / 2] + (m / FN * 4 + h * 2 + m % 2) * eight_rows);
   };
 
   auto pin = [&]() {  // (else the compiler moves the matrix instructions of a half past the branches after it)
@@ -588,8 +588,9 @@ __device__ __forceinline__ void stream_tiles(const GroupedMxParams& p, uint8_t* 
     const int nc = (int)min(p.N - n0, (int64_t)256);
     // (the descriptor ends with the tile's last row: rows past it are not stored)
     ro = descriptor(reinterpret_cast<uint16_t*>(p.c) + (int64_t)m0 * p.ldc + n0, (int)((mr - 1) * p.ldc + nc) * 2);
-    left = nc - col;
-    vo = (uint32_t)(wm * 128 + (lane & 7)) * (uint32_t)(p.ldc * 2) + col * 2;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)  // (no column: past the descriptor's end whatever rows are added)
+      vo[c] = 64 * c < nc - col ? (uint32_t)(wm * 128 + (lane & 7)) * (uint32_t)(p.ldc * 2) + (64 * c + col) * 2 : kNoElement;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       f32x16& v = acc[m / FN][m % FN];
