@@ -526,6 +526,8 @@ mxf_status mxfp4_dequantize(const mxf_operand_desc* desc /* host */, const void*
  * exact, and each enters the FP32 accumulator with 2^-23 of it lost at most (E4M3: two sums, of the products with codes of
  * magnitudes from 2 on and of those with smaller ones).
  * A group with scale byte 0xFF makes NaN of the outputs that it enters.
+ * Limits: E, M, N and K as for grouped_gemm_*; (M / 128 + min(E, M)) ceil(N / 256) (forward) or E ceil(N / 128) ceil(K / 256)
+ * (wgrad) below 2^24.
  * desc: as grouped_gemm_*, flags MXF_GROUPED_OUT_F32 | MXF_GROUPED_ACCUM (wgrad) | MXF_GROUPED_LEFT_E4M3; ldy is y's row stride
  * (forward); ldx is not used. Codes 16-byte aligned, scales 4; y and dw aligned to their elements. offs on the device, its
  * contract and *status as for grouped_gemm_*; rows at or past offs[E] are never written.

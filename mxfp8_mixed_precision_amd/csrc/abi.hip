@@ -1110,6 +1110,12 @@ static mxf_status run_grouped_mx(bool wgrad, const char* name, const mxf_grouped
     return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
   if ((d->flags & MXF_GROUPED_ACCUM) && (!wgrad || !(d->flags & MXF_GROUPED_OUT_F32)))
     return fail(MXF_E_ARG, "flags = 0x%x: MXF_GROUPED_ACCUM is for wgrad with MXF_GROUPED_OUT_F32", d->flags);
+  // (where there are many, tiles are 128 x 256, and every expert may end inside one)
+  const int64_t ct = ((wgrad ? d->K : d->N) + 255) / 256;
+  const int64_t rt = wgrad ? d->E * ((d->N + 127) / 128) : d->M / 128 + (d->E < d->M ? d->E : d->M);
+  if (rt > kMostBlocks / ct)
+    return fail(MXF_E_SHAPE, "E = %d, M = %lld, N = %lld, K = %lld: more than 2^24 tiles", d->E, (long long)d->M,
+                (long long)d->N, (long long)d->K);
   if (!offs) return fail(MXF_E_NULL, "offs is NULL");
   if (!aligned4(offs) || !aligned4(status)) return fail(MXF_E_ALIGN, "offs or status is not 4-byte aligned");
   const bool rows = d->M > 0;  // without rows the operands may be NULL
@@ -1120,12 +1126,6 @@ static mxf_status run_grouped_mx(bool wgrad, const char* name, const mxf_grouped
   if ((s = check_operand_ptrs(a, as, wgrad ? "dy" : "x")) != MXF_OK || (s = check_operand_ptrs(b, bs, wgrad ? "x" : "w")) != MXF_OK)
     return s;
   if (!aligned_to(out, f32 ? 4 : 2)) return fail(MXF_E_ALIGN, "the output is not aligned to its elements");
-  // (the few-rows kernel's strips of 32 columns, up to two tiles of rows for each expert, are the finest grid)
-  const int64_t ct = wgrad ? (d->K + 127) / 128 : (d->N + 31) / 32;
-  const int64_t rt = wgrad ? d->E * ((d->N + 127) / 128) : d->M / 32 + d->E;
-  if (rt > kMostBlocks / ct)
-    return fail(MXF_E_SHAPE, "E = %d, M = %lld, N = %lld, K = %lld: more than 2^24 tiles", d->E, (long long)d->M,
-                (long long)d->N, (long long)d->K);
   if ((s = check_device()) != MXF_OK) return s;
   int ncu = 0;
   if ((s = cu_count(&ncu)) != MXF_OK) return s;
