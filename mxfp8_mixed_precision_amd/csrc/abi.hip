@@ -901,9 +901,6 @@ mxf_status grouped_gemm_wgrad(const mxf_grouped_desc* desc, const int32_t* offs,
 
 // ------------------------------------------------------------------ token rows to experts and back
 
-// Blocks of a launch: a kernel's grid holds fewer than 2^24 blocks of 256 threads.
-constexpr int64_t kMostBlocks = 0xFFFFFF;
-
 static mxf_status check_route_desc(const mxf_route_desc* d, uint32_t flags) {
   if (!d) return fail(MXF_E_NULL, "desc is NULL");
   mxf_status st = check_plan_sizes(d->tokens, d->topk, d->E);
@@ -915,9 +912,10 @@ static mxf_status check_route_desc(const mxf_route_desc* d, uint32_t flags) {
     return fail(MXF_E_SHAPE, "ldx = %lld, ldh = %lld: must be at least D (%lld)", (long long)d->ldx, (long long)d->ldh,
                 (long long)d->D);
   if (d->flags & ~flags) return fail(MXF_E_ARG, "flags = 0x%x: unknown bits", d->flags);
-  if (d->tokens * ((d->D + 127) / 128) / 4 + d->rows / 64 + 2 > kMostBlocks)
-    return fail(MXF_E_SHAPE, "tokens = %lld, rows = %lld, D = %lld: too many blocks", (long long)d->tokens,
-                (long long)d->rows, (long long)d->D);
+  // (so that the blocks of a launch, four spans of a row or a token each and the pad rows', are counted in 32 bits)
+  if (d->tokens * ((d->D + 127) / 128) > ((int64_t)1 << 33))
+    return fail(MXF_E_SHAPE, "tokens = %lld, D = %lld: tokens * ceil(D / 128) must be at most 2^33", (long long)d->tokens,
+                (long long)d->D);
   return MXF_OK;
 }
 
@@ -1014,6 +1012,9 @@ mxf_status mxf_combine_bwd(const mxf_route_desc* d, const int32_t* offs, const i
 }
 
 // ------------------------------------------------------------------ MXFP4 operands and products
+
+// Blocks of a launch: a kernel's grid holds fewer than 2^24 blocks of 256 threads.
+constexpr int64_t kMostBlocks = 0xFFFFFF;
 
 static mxf_status check_operand_desc(const mxf_operand_desc* d) {
   if (!d) return fail(MXF_E_NULL, "desc is NULL");

@@ -28,6 +28,9 @@ namespace mxf {
 constexpr int kPadRows = 16;  // rows of row_assign per wavefront
 constexpr int kRowsInFlight = 8;
 
+// (rows of a grid of more than one are equally long)
+__device__ __forceinline__ unsigned block_of_grid() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // The expert row of assignment a, -1 if it has none.
 __device__ __forceinline__ int64_t row_of(const RouteParams& p, int64_t a) {
   const int32_t r = p.assign_row[a];
@@ -71,12 +74,13 @@ __device__ __forceinline__ void zero_pads(const RouteParams& p, uint8_t* out, in
 template <int LPT>
 __global__ __launch_bounds__(256) void dispatch_kernel(RouteParams p, unsigned pad_blocks, int spans) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned block = block_of_grid();
   uint8_t* out = reinterpret_cast<uint8_t*>(p.h);
-  if (blockIdx.x < pad_blocks) {
-    zero_pads(p, out, p.D, p.ldh, ((int64_t)blockIdx.x * 4 + w) * kPadRows);
+  if (block < pad_blocks) {
+    zero_pads(p, out, p.D, p.ldh, ((int64_t)block * 4 + w) * kPadRows);
     return;
   }
-  const int64_t wave = (int64_t)(blockIdx.x - pad_blocks) * 4 + w;
+  const int64_t wave = (int64_t)(block - pad_blocks) * 4 + w;
   const int64_t t = LPT == 64 ? wave / spans : wave * (64 / LPT) + lane / LPT;
   if (t >= p.tokens) return;
   const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) + t * p.ldx;
@@ -109,7 +113,7 @@ template <class T, int LPT, bool W, bool ONCE>
 __global__ __launch_bounds__(256) void combine_kernel(RouteParams p, int spans) {
   constexpr int VEC = Elem<T>::VEC;
   const int lane = threadIdx.x & 63;
-  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t wave = (int64_t)block_of_grid() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = LPT == 64 ? wave / spans : wave * (64 / LPT) + lane / LPT;
   if (t >= p.tokens) return;
   const T* h = reinterpret_cast<const T*>(p.h);
@@ -165,12 +169,14 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(RouteParams p, unsigne
   constexpr int VEC = Elem<T>::VEC, TPB = 256 / LPT, WPT = LPT / 64;
   __shared__ float red[DOT && WPT > 1 ? 4 * kRowsInFlight : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (blockIdx.x < pad_blocks) {
+  const unsigned block = block_of_grid();
+  if (block < pad_blocks) {
     zero_pads(p, reinterpret_cast<uint8_t*>(p.dh), p.D * sizeof(T), p.lddh * sizeof(T),
-              ((int64_t)blockIdx.x * 4 + wave) * kPadRows);
+              ((int64_t)block * 4 + wave) * kPadRows);
     return;
   }
-  int64_t t = (int64_t)(blockIdx.x - pad_blocks) * TPB;
+  int64_t t = (int64_t)(block - pad_blocks) * TPB;
+  if (t >= p.tokens) return;
   if constexpr (WPT > 0)
     t += wave / WPT;
   else
@@ -259,8 +265,13 @@ namespace {
 
 // Lanes that hold a row of `chunks` 16-byte chunks: a power of two from 8 to 64.
 int lanes_per_token(int64_t chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64; }
-unsigned blocks_of(int64_t waves) { return (unsigned)((waves + 3) / 4); }
-unsigned blocks_of_pads(int64_t rows) { return blocks_of((rows + mxf::kPadRows - 1) / mxf::kPadRows); }
+int64_t blocks_of(int64_t waves) { return (waves + 3) / 4; }
+int64_t blocks_of_pads(int64_t rows) { return blocks_of((rows + mxf::kPadRows - 1) / mxf::kPadRows); }
+// A row of a grid holds fewer than 2^24 blocks of 256 threads; the blocks of the last row that are too many find no token.
+dim3 grid_of(int64_t blocks) {
+  constexpr int64_t kRow = 0xFFFFFF;
+  return blocks <= kRow ? dim3((unsigned)blocks) : dim3((unsigned)kRow, (unsigned)((blocks + kRow - 1) / kRow));
+}
 
 // Whether h (`copies` 2: and dh) fills most of the 256 MB last-level cache, so that none of it is still there: it is read past the caches
 // then, where its rows are whole 128-byte lines (a line that two instructions share would come twice).
@@ -285,7 +296,7 @@ hipError_t launch_combine(const mxf::RouteParams& p, hipStream_t st) {
   return with_lanes(chunks, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
     const int64_t waves = L == 64 ? p.tokens * spans : (p.tokens + 64 / L - 1) / (64 / L);
-    hipLaunchKernelGGL((mxf::combine_kernel<T, L, W, ONCE>), dim3(blocks_of(waves)), dim3(256), 0, st, p, (int)spans);
+    hipLaunchKernelGGL((mxf::combine_kernel<T, L, W, ONCE>), grid_of(blocks_of(waves)), dim3(256), 0, st, p, (int)spans);
     return hipGetLastError();
   });
 }
@@ -295,9 +306,8 @@ hipError_t launch_combine_bwd(const mxf::RouteParams& p, hipStream_t st) {
   const int64_t chunks = (p.D + mxf::Elem<T>::VEC - 1) / mxf::Elem<T>::VEC;
   const auto go = [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const unsigned tb = (unsigned)((p.tokens + 256 / L - 1) / (256 / L));
-    const unsigned pads = blocks_of_pads(p.rows);
-    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L, DOT, ONCE>), dim3(pads + tb), dim3(256), 0, st, p, pads);
+    const int64_t tb = (p.tokens + 256 / L - 1) / (256 / L), pads = blocks_of_pads(p.rows);
+    hipLaunchKernelGGL((mxf::combine_bwd_kernel<T, L, DOT, ONCE>), grid_of(pads + tb), dim3(256), 0, st, p, (unsigned)pads);
     return hipGetLastError();
   };
   // A block per token for long rows, or few tokens (us with a wavefront per token): 4096 tokens of 8 rows of 7168 BF16 207, 215; of 6
@@ -313,10 +323,9 @@ hipError_t mxf_launch_dispatch(const mxf::RouteParams& p, hipStream_t st) {
   const int64_t chunks = (p.D + 15) / 16, spans = (chunks + 63) / 64;
   return with_lanes(chunks, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const unsigned tb = blocks_of(L == 64 ? p.tokens * spans : (p.tokens + 64 / L - 1) / (64 / L));
-    const unsigned pads = blocks_of_pads(p.rows);
+    const int64_t tb = blocks_of(L == 64 ? p.tokens * spans : (p.tokens + 64 / L - 1) / (64 / L)), pads = blocks_of_pads(p.rows);
     if (pads + tb == 0) return hipSuccess;
-    hipLaunchKernelGGL((mxf::dispatch_kernel<L>), dim3(pads + tb), dim3(256), 0, st, p, pads, (int)spans);
+    hipLaunchKernelGGL((mxf::dispatch_kernel<L>), grid_of(pads + tb), dim3(256), 0, st, p, (unsigned)pads, (int)spans);
     return hipGetLastError();
   });
 }

@@ -6,7 +6,7 @@ import torch
 import mxfp8_mixed_precision_amd as mx
 from gpu_util import require_gpu
 from mxfp8_mixed_precision_amd import _abi
-from test_expert_abi import P, grouped, refused
+from test_expert_abi import P, grouped, refused, route
 from test_gpu_grouped_mx import close, operand, values
 
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that a kernel must not reach")
@@ -27,6 +27,55 @@ def test_forward_products(kw, inside):
     (dict(E=512, N=32768, K=32768), False)])
 def test_weight_gradients(kw, inside):
     assert (refused(mx.mxf_grouped_gemm_mxfp4_wgrad, grouped(**kw), P, P, P, P, P, P) != _abi.E_SHAPE) == inside
+
+
+@no_gpu
+@pytest.mark.parametrize("tokens,D,topk,inside", [(1 << 20, 8192, 1, True), (1 << 29, 1, 2, True), (1 << 30, 1024, 1, True), (1 << 24, 65536, 64, True),
+                                                  (1 << 30, 1025, 1, False), (1 << 24, 65537, 64, False)])
+def test_rows_of_tokens(tokens, D, topk, inside):
+    d = route(tokens=tokens, D=D, ldx=D, ldh=D, lddh=D, topk=topk, rows=1 << 30)
+    for fn, n in ((mx.mxf_dispatch_fwd, 5), (mx.mxf_combine_bwd, 8)):
+        assert (refused(fn, d, *[P] * n) != _abi.E_SHAPE) == inside
+    assert (refused(mx.mxf_combine_fwd, d, P, P, P, None, P) != _abi.E_SHAPE) == inside
+
+
+@pytest.mark.gpu
+def test_rows_in_more_blocks_than_a_row_of_the_grid():
+    """2^29 - 2^20 tokens of one element, two rows each, and 2^21 pad rows."""
+    require_gpu()
+    T, R = (1 << 29) - (1 << 20), 1 << 30
+    i32 = dict(dtype=torch.int32, device="cuda")
+    row = torch.arange(2 * T, **i32) ^ 0x15555  # its own inverse
+    plan = {"offs": torch.tensor([0, R], **i32), "row_assign": torch.cat([row, torch.full((R - 2 * T,), -1, **i32)]), "assign_row": row}
+    x = torch.randint(1, 100, (T, 1), dtype=torch.uint8, device="cuda")
+    xe = mx.dispatch_fwd(x, plan)
+    assert torch.equal(xe[:2 * T], x[row.long() // 2]) and not xe[2 * T:].any()
+    h, dy, w = xe.bfloat16(), x.bfloat16(), torch.full((T, 2), 0.5, dtype=torch.bfloat16, device="cuda")
+    w[:, 1] = 2
+    del xe
+    assert torch.equal(mx.combine_fwd(h, w, plan), (2.5 * x.float()).bfloat16())
+    assert torch.equal(mx.dispatch_bwd(h, plan, T), 2 * dy)
+    dh, dw = mx.combine_bwd(dy, h, w, plan)
+    assert torch.equal(dh[:2 * T], (dy[row.long() // 2] * w.view(-1)[row.long()][:, None])) and not dh[2 * T:].any()
+    assert torch.equal(dw, x.float().square().expand(T, 2))
+
+
+@pytest.mark.gpu
+def test_many_wide_rows():
+    """2^20 tokens of 8192."""
+    require_gpu()
+    T, D = 1 << 20, 8192
+    i32 = dict(dtype=torch.int32, device="cuda")
+    row = torch.arange(T, **i32) ^ 0x5555
+    plan = {"offs": torch.tensor([0, T], **i32), "row_assign": row, "assign_row": row}
+    x = torch.randint(0, 100, (T, D), dtype=torch.int16, device="cuda").bfloat16()
+    w = torch.full((T, 1), 0.5, device="cuda")
+    xe = mx.dispatch_fwd(x, plan)
+    assert torch.equal(xe, x[row.long()])
+    assert torch.equal(mx.combine_fwd(xe, w, plan), 0.5 * x)
+    dh, dw = mx.combine_bwd(x, xe, w, plan)
+    assert torch.equal(dh, 0.5 * xe)
+    assert (dw[:, 0].double() - torch.stack([v.double().square().sum(1) for v in x.split(1 << 16)]).view(-1)).abs().max() <= D * 2.0 ** -24 * D * 1e4
 
 
 @pytest.mark.gpu
