@@ -443,8 +443,8 @@ mxf_status grouped_gemm_wgrad(const mxf_grouped_desc* desc /* host */, const int
  * Limits: tokens * topk <= 2^30, 1 <= topk <= 64, 0 <= rows <= 2^30, 1 <= D <= 2^20, tokens * ceil(D / 128) <= 2^33,
  * 1 <= E <= 1024, strides >= D.
  * Pointers aligned to their elements, int32 arrays to 4; any width and alignment goes at the same rate. Without tokens the
- * token side, without rows the row side may be NULL. Outputs may not overlap inputs.
- * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags, element), MXF_E_DEVICE, MXF_E_HIP. Profiling names
+ * token side, without rows the row side may be NULL. Outputs may not overlap inputs; residual == y is refused.
+ * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags, element, residual), MXF_E_DEVICE, MXF_E_HIP. Profiling names
  * dispatch, combine_fwd, combine_bwd. */
 #define MXF_ROUTE_F32 1u         /* x, h, y, dy, dh are FP32 instead of BF16 */
 #define MXF_ROUTE_WEIGHT_F32 2u  /* weights are FP32 instead of BF16 */

@@ -972,6 +972,7 @@ mxf_status mxf_combine_fwd(const mxf_route_desc* d, const int32_t* assign_row, c
   const size_t n = f32 ? 4 : 2;
   if (!assign_row || !y || (d->rows > 0 && !h)) return fail(MXF_E_NULL, "assign_row, h or y is NULL");
   if (!aligned4(assign_row)) return fail(MXF_E_ALIGN, "assign_row is not 4-byte aligned");
+  if (residual == y) return fail(MXF_E_ARG, "residual is y: it has to be a tensor of its own");
   if (!aligned_to(h, n) || !aligned_to(y, n) || !aligned_to(residual, n) ||
       !aligned_to(weights, (d->flags & MXF_ROUTE_WEIGHT_F32) ? 4 : 2))
     return fail(MXF_E_ALIGN, "h, y, residual or weights is not aligned to its elements");

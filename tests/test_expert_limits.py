@@ -39,6 +39,14 @@ def test_rows_of_tokens(tokens, D, topk, inside):
     assert (refused(mx.mxf_combine_fwd, d, P, P, P, None, P) != _abi.E_SHAPE) == inside
 
 
+@no_gpu
+def test_a_residual_in_the_result_s_place():
+    """The last two chunks of a row overlap: a row would be read where it is written."""
+    assert refused(mx.mxf_combine_fwd, route(), P, P, P, P << 1, P << 1) == _abi.E_ARG
+    assert refused(mx.mxf_combine_fwd, route(), P, P, None, P << 1, P << 1) == _abi.E_ARG
+    assert refused(mx.mxf_combine_fwd, route(), P, P, P, P << 2, P << 1) not in (_abi.E_ARG, _abi.E_SHAPE, _abi.E_ALIGN, _abi.E_NULL)
+
+
 @pytest.mark.gpu
 def test_rows_in_more_blocks_than_a_row_of_the_grid():
     """2^29 - 2^20 tokens of one element, two rows each, and 2^21 pad rows."""
