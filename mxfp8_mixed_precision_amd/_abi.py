@@ -292,7 +292,7 @@ def mxf_route_plan_noalloc(expert_idx, tokens, topk, E, pad_multiple, m_capacity
 
 def route_plan(expert_idx, E, pad_multiple, m_capacity, stream=None):
     """Routing plan of expert ids [tokens, topk] (int32 CUDA tensor); allocates and returns
-    dict(offs, counts, row_assign, assign_row, status) as int32 CUDA tensors."""
+    dict(offs, counts, row_assign, assign_row, status) as int32 CUDA tensors, and topk."""
     import torch
     assert expert_idx.dtype == torch.int32 and expert_idx.dim() == 2 and expert_idx.is_contiguous()
     tokens, topk = expert_idx.shape
@@ -307,6 +307,7 @@ def route_plan(expert_idx, E, pad_multiple, m_capacity, stream=None):
                    out["row_assign"], out["assign_row"], out["status"], ws, stream)
     out["row_assign"] = out["row_assign"][:m_capacity]
     out["assign_row"] = out["assign_row"][:tokens * topk]
+    out["topk"] = topk
     return out
 
 

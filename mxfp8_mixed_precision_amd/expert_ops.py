@@ -5,7 +5,8 @@ As in block_ops.py each call checks its tensors (ValueError), allocates its outp
 (MxfError) on the current stream of the tensors' device, or on ``stream=``.
 
 ``plan`` is what ``route_plan`` returns: a dict with int32 tensors offs [E + 1], row_assign [rows] and assign_row [tokens *
-topk]. Rows at or past offs[E] of an output with expert rows are left as allocated.
+topk], and topk, which a call's number of tokens has to match (a plan made elsewhere may lack it: then it is assignments over
+tokens). Rows at or past offs[E] of an output with expert rows are left as allocated.
 
 An MXFP4 operand of a matrix [rows, K] is a pair (q, s): uint8 codes [P, rows, 64] and scale bytes [P, rows, 4], P = ceil(K /
 128); with E4M3 elements q is [2 P, rows, 64]. K is padded with zeros, so only P is left of it. A batch of matrices has
@@ -32,10 +33,17 @@ def _plan(plan, device, rows=None):
     return plan["offs"], plan["row_assign"], plan["assign_row"]
 
 
-def _topk(assign_row, tokens):
-    n = assign_row.numel()
+def _topk(plan, tokens):
+    """Experts per token: the plan's own where it has them, else assignments over tokens."""
+    n, topk = plan["assign_row"].numel(), plan.get("topk")
     if tokens < 0:
         _bad(f"{tokens} tokens")
+    if topk is not None:
+        if topk < 1:
+            _bad(f"plan: topk = {topk}")
+        if tokens * topk != n:
+            _bad(f"plan: {n} assignments, {topk} per token, are not of {tokens} tokens")
+        return topk
     if tokens == 0:
         if n:
             _bad(f"plan: {n} assignments of no tokens")
@@ -62,7 +70,7 @@ def dispatch_fwd(x, plan):
     tokens, D, ld = _rows(x, "x")
     dev = x.device
     offs, row_assign, assign_row = _plan(plan, dev)
-    topk, rows = _topk(assign_row, tokens), row_assign.numel()
+    topk, rows = _topk(plan, tokens), row_assign.numel()
     xe = torch.empty((rows, D), dtype=x.dtype, device=dev)
     _run("mxf_dispatch_fwd", RouteDesc(tokens, rows, D, ld, D, D, topk, offs.numel() - 1, x.element_size(), 0),
          offs.data_ptr(), row_assign.data_ptr(), assign_row.data_ptr(), x.data_ptr(), xe.data_ptr(), _stream_of(dev))
@@ -74,7 +82,7 @@ def _combine(h, weights, plan, tokens, residual=None):
     rows, D, ld = _rows(h, "h")
     dev = h.device
     offs, _, assign_row = _plan(plan, dev, rows)
-    topk = _topk(assign_row, tokens)
+    topk = _topk(plan, tokens)
     flags = _float_flag(h, "h")
     if weights is not None:
         flags |= 2 * _float_flag(weights, "weights")
@@ -120,7 +128,7 @@ def combine_bwd(dy, h, weights, plan):
             _bad("h and dy differ in type or width")
         _on(h, dev, "h")
     offs, row_assign, assign_row = _plan(plan, dev, rows)
-    rows, topk = row_assign.numel(), _topk(assign_row, tokens)
+    rows, topk = row_assign.numel(), _topk(plan, tokens)
     if weights is None or weights.dim() != 2:
         _bad("weights [tokens, topk] are needed")
     flags = _float_flag(dy, "dy") | 2 * _float_flag(weights, "weights")
@@ -161,8 +169,8 @@ def mxfp4_quantize(x, mode=_abi.ROW, e4m3=False, plan=None):
     else:
         rows, cols, ld = _rows(x, "x")
         if plan is not None:
-            offs, row_assign, assign_row = _plan(plan, dev)
-            tokens, topk, E = rows, _topk(assign_row, rows), offs.numel() - 1
+            offs, row_assign, _ = _plan(plan, dev)
+            tokens, topk, E = rows, _topk(plan, rows), offs.numel() - 1
             rows = row_assign.numel()
     q = s = qt = st = None
     if mode & _abi.ROW:
