@@ -515,9 +515,8 @@ __device__ __forceinline__ void stream_tiles(const GroupedMxParams& p, uint8_t* 
 #pragma unroll
     for (int m = 0; m < NM; ++m) asm volatile("" : "+a"(acc[m / FN][m % FN]));
   };
-  auto stage = [&](auto pre_, int kt, uint32_t& slot, uint32_t& last) {
+  auto stage = [&](auto pre_, uint32_t& slot, uint32_t& last) {
     constexpr int pre = decltype(pre_)::value;  // the stores' share of this stage, -1 none
-    (void)kt;
     // first half, beside the reads of the second, the rest of the loads of the stage that took the last slot, and stores
     each<NM>([&](auto m_) {
       constexpr int m = decltype(m_)::value, l0 = LH + m * (T::L - LH) / NM, l1 = LH + (m + 1) * (T::L - LH) / NM;
@@ -577,9 +576,9 @@ __device__ __forceinline__ void stream_tiles(const GroupedMxParams& p, uint8_t* 
   uint32_t slot = 0, last = (S - 1) * T::STAGE;
 #pragma unroll 1
   for (int t = 0; t < n; ++t) {
-    each<PRE>([&](auto k) { stage(k, 0, slot, last); });
+    each<PRE>([&](auto k) { stage(k, slot, last); });
 #pragma unroll 1
-    for (int kt = PRE; kt < KT; ++kt) stage(std::integral_constant<int, -1>(), kt, slot, last);
+    for (int kt = PRE; kt < KT; ++kt) stage(std::integral_constant<int, -1>(), slot, last);
     // pack: accumulators 4 c .. 4 c + 3 are row r32, columns 8 c + 4 g and the next three; the halves of the wavefront exchange so
     // that a lane has eight columns in a row, then its quarters (64 bytes of 16 rows), then eights of neighbouring fragments: a
     // store has 128 bytes of 8 rows
