@@ -397,7 +397,8 @@ mxf_status mxf_swiglu_ckpt_bwd(const void* dh, int64_t lddh, const void* q, cons
  * With few rows per expert the weights' bytes bound a product: fwd then streams the weight of each expert
  * that has rows once (more than 32 rows of one read it again from the cache), and wgrad writes dw at the rate of
  * stores.
- * Limits: E in [1, 1024]; M in [0, 2^30]; N, K in [1, 2^20]; ldx >= K, ldy >= N. Pointers aligned to
+ * Limits: E in [1, 1024]; M in [0, 2^30]; N, K in [1, 2^20]; fewer than 2^24 tiles of 128 x 128 (rows: M / 128 + E;
+ * wgrad: N for each expert); ldx >= K, ldy >= N. Pointers aligned to
  * their elements, int32 arrays to 4; operands and outputs whose rows are 16-byte aligned (N, K, ldx, ldy
  * multiples of 8; wgrad from codes: K a multiple of 16 and aligned codes) take the fast kernels: the others
  * need about twice the time (fwd of few rows: 4-byte alignment is enough). Outputs may not overlap inputs.
@@ -493,7 +494,8 @@ mxf_status mxf_combine_bwd(const mxf_route_desc* desc /* host */, const int32_t*
  * written).
  * mxfp4_dequantize: out [batch][rows, cols] dense, BF16 or FP32 (MXF_OPERAND_F32), of an operand along its rows: element times
  * scale, rounded once. (The operand of a transposed matrix reads back transposed.)
- * Limits: 0 <= batch, rows <= 2^30, 1 <= cols <= 2^20, fewer than 2^24 tiles of 128 x 128; cols <= ldx <= 2^32. x, out aligned to their elements; codes 16 bytes, scales 4. Nothing to do without batch or rows.
+ * Limits: 0 <= batch, rows <= 2^30, 1 <= cols <= 2^20, fewer than 2^24 tiles of 128 x 128; cols <= ldx <= 2^32. x, out
+ * aligned to their elements; codes 16 bytes, scales 4. Nothing to do without batch or rows.
  * Errors: MXF_E_NULL, MXF_E_SHAPE, MXF_E_ALIGN, MXF_E_ARG (flags), MXF_E_DEVICE, MXF_E_HIP. Profiling names
  * mxfp4_quantize, mxfp4_dequantize. */
 #define MXF_OPERAND_F32 1u   /* the matrix is FP32 instead of BF16 */

@@ -15,6 +15,7 @@
 // Bound by HBM (copy: 6.1 TB/s; BF16): dispatch of 4096 tokens to 24576 rows of 2048 and the padding 20.6 us (127 MB, 5.9 TB/s;
 // by whole tokens 25.7); combine back 18.2 (119 MB, 6.1 TB/s); gradient of 4096 tokens, 32768 rows of 7168 and the padding 191
 // (1057 MB, 5.5 TB/s; h through the caches 206, with 64 lanes per token, which hold a row's chunks one after the other, 220).
+// Dispatch's gradient of 4096 tokens of 6 rows of 2048 18.1 (119 MB), of 8 of 7168 97 (531 MB, 5.5 TB/s).
 // Combine of 8 tokens: 3.9.
 //
 // A row's last chunk is taken from its end backwards, over elements that its neighbour has too: both store the same
@@ -332,7 +333,7 @@ hipError_t mxf_launch_dispatch(const mxf::RouteParams& p, hipStream_t st) {
 
 hipError_t mxf_launch_combine(const mxf::RouteParams& p, bool f32, hipStream_t st) {
   // (us, through the caches): 4096 tokens of 8 rows of 7168 BF16 89, 96; of 6 rows of 2048 FP32 40, 43.5; but 8192 tokens of 4
-  // rows of 1411 BF16 21.5, 20
+  // rows of 1411 BF16 21.5, 20. Without weights (dispatch's gradient) h goes through the caches; the other way was not measured.
   if (p.w && read_once(p, f32 ? 4 : 2, 1))
     return f32 ? launch_combine<float, true, true>(p, st) : launch_combine<uint16_t, true, true>(p, st);
   if (p.w) return f32 ? launch_combine<float, true, false>(p, st) : launch_combine<uint16_t, true, false>(p, st);

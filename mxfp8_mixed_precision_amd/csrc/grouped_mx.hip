@@ -37,8 +37,8 @@ __device__ __forceinline__ int large_codes(int v) {
 // Rows that do not exist load as zeros (bounded loads), the contraction is padded by the layout.
 //
 // Measured (us; instructions alone at 7.2 PFLOP/s, E4M3 x E2M1 4.6): weight gradient of 24576 x 2816 x 2048, 16 experts, into FP32 114
-// (compute 40, the 369 MB of stores 61, one after the other in a tile; into BF16 94); forward of 24576 x 2816 x 2048 with E4M3
-// rows 205 (instructions 123; with one product for all codes, right to 4e-5 alone, 130).
+// (compute 40, the 369 MB of stores 61, one after the other in a tile; into BF16 94, added to FP32 251); forward of 24576 x 2816 x
+// 2048 with E4M3 rows 192-205 (instructions 123, matrix cores busy 72%), 8192^3 632-686 (478, 86%).
 template <int BM, int BN, bool A8, int S_>
 struct MxTile {
   static constexpr int S = S_;
@@ -381,9 +381,11 @@ __global__ __launch_bounds__(256, OCC) void grouped_mx_rows_kernel(GroupedMxPara
 // at the memory's rate. Stores are whole 128-byte lines past the caches (64-byte halves or cached lines: 97 us for 85 below), two to
 // each of 16 stages, or four to each of 8 where a tile has fewer than 16.
 //
-// 24576 x 2816 x 2048, 16 experts, 85 us (3.3 PFLOP/s; tiles one by one 90, compute 40 at the instructions' rate): a tile is 16
-// stages, and the chip stores 138 MB at the same time. 16384 x 4096 x 7168, 8 experts, 224-240 us (4.0-4.3 PFLOP/s), 8192^3 235 (4.7):
-// matrix cores busy 58% of the cycles at 1.73 GHz, to which the power limit lowers the clock (2.4 without load).
+// 24576 x 2816 x 2048, 16 experts, 83-86 us (3.3 PFLOP/s; tiles one by one 90, compute 40 at the instructions' rate): a tile is 16
+// stages, the chip stores 138 MB at the same time, and the matrix cores are busy 40% of the cycles. 16384 x 4096 x 7168, 8 experts,
+// 230-237 us (4.1 PFLOP/s), 8192^3 231 (4.7): busy 58% and 66% of the cycles. These run at 1.7 GHz, as the instructions alone do (2.4
+// without load), so what is left is cycles without a matrix instruction: one wavefront to a SIMD waits, at barriers and for LDS, 20%
+// of its time, and nothing else can issue meanwhile.
 constexpr int kStreamTiles = 1024;  // of a block: its list is in LDS
 
 struct StreamTile {

@@ -17,10 +17,11 @@
 // of codes, 512 bytes of scales), put together in LDS. A tile's amax takes four exchanges of packed pairs for the columns and two for
 // the rows. BF16 values go through in pairs (v_cvt_scalef32_pk_fp4_bf16, 16-bit magnitudes), FP32 ones one by one.
 //
-// FP32 is bound by HBM: 16 weights of 2816 x 2048, rows 71 us (5.7 TB/s), and as BF16 read back 34 (6.6 TB/s). BF16 in both
-// directions is not: 24576 x 2048 28.4, rows alone 23.9 (6.3 TB/s). Gathered rows (a plan's, topk 6) would be read topk times
-// from memory where neighbouring tiles of a row land on different XCDs; each XCD takes a run of row tiles, whose rows are in its L2 for
-// all their columns: 25.0 us for 24576 x 2048 in both directions, 18 MB read.
+// FP32 is bound by HBM: 16 weights of 2816 x 2048, rows 76 us (418 MB, 5.5 TB/s), and as BF16 read back 35 (235 MB, 6.6 TB/s). BF16
+// is not: 24576 x 2048 rows 24.8 (127 MB, 5.1 TB/s), in both directions 28.7. Gathered rows (a plan's, topk 6) would be read topk times
+// from memory where a token's experts' rows land on different XCDs; each XCD takes few column tiles of all rows, whose piece of x its
+// L2 then holds: 25.4 us for 24576 x 2048 in both directions, 18 MB read, 58 written; the vector instructions are issued 64% of the
+// time (the codes and two amax exchanges), LDS is busy 11%, a quarter of it with conflicts.
 #include "chunk.h"
 #include "kernels.h"
 #include "ragged.h"
