@@ -845,11 +845,12 @@ hipError_t launch(bool wgrad, const GroupedMxParams& p, int ncu, hipStream_t st)
   // share it (us, in tiles): one row 4096 x 4096 4.0, 10.1; 4 experts of 4096 x 4096, 8 rows each 8.4, 10.6; one expert of 1024
   // x 8192, 200 rows 7.3, 17.1; 32 experts of 300 x 7168, 3 rows each 10.8, 15.5. With more blocks a strip's own cost weighs more: 16
   // experts of 2816 x 2048, 32 rows each 13.8, 12.2; 256 experts, 1 row each 212, 161.
-  // E4M3 rows, whose instructions cost twice as much, share a long contraction out further, and with few rows to an expert for any
-  // number of strips (us, in tiles): 16 experts of 2816 x 2048, 3 rows each 12.6, 14.4, 32 rows each 18.0, 14.6; 64 experts, 3 rows
-  // each 45.8, 67, 16 rows each 68.7, 68.4; 64 experts of 2048 x 1408, 4 rows each 28.5, 32.2; but of 1024 x 512 11.6, 10.5.
+  // E4M3 rows, whose instructions cost twice as much, share a long contraction out further (us, in tiles): 16 experts of 2816 x 2048, 3
+  // rows each 12.6, 14.4, 32 rows each 18.0, 14.6; 256 rows of 4096 x 4096 16.3, 26.7, of 8192 x 8192 58, 49; and with few rows to an
+  // expert still further: 64 experts, 3 rows each 45.8, 67, 16 rows each 68.7, 68.4; 2048 x 1408, 4 rows each 28.5, 32.2, of 1024
+  // x 512 11.6, 10.5; but 256 experts of 2048 x 1408 with 2 rows each 157, 81, as blocks without rows cost too.
   const int64_t fct = (p.N + FC - 1) / FC, frt = p.M / FR + met, fs = frt * ((p.N + 127) / 128);
-  if (!wgrad && (fs <= 3 * ncu / 4 || (A8 && p.K > 1024 && (fs <= 7 * ncu / 4 || p.M <= 8 * met) && frt * fct < (1 << 23)))) {
+  if (!wgrad && (fs <= 3 * ncu / 4 || (A8 && p.K > 1024 && (fs <= 7 * ncu / 4 || (p.M <= 8 * met && fs <= 8 * ncu))))) {
     hipLaunchKernelGGL(grouped_mx_few_rows_kernel<A8>, dim3((unsigned)(frt ? frt * fct : 1)), dim3(64 * FW), 0, st, p, (int)fct);
     return hipGetLastError();
   }
