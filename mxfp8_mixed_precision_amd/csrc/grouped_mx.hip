@@ -173,6 +173,9 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
   // beside which the next fragment's large ones are (always after the product, which would wait for them). LIVE: fragments
   // that have rows.
   constexpr int PARTS = A8 ? 2 : 1;
+  // the order as written, but for E4M3 on 128 x 128 tiles, few of which have a second wavefront to fill the gaps (one expert, 256 rows of
+  // 8192 x 8192 43.8 us against 49.4; on 128 x 256 tiles 208 against 203 at 24576 x 2816 x 2048)
+  constexpr bool FIXED = !(A8 && FN == 2);
   i32x8 part[2];
   auto multiply = [&](auto m_, auto ks_, auto live_) {
     constexpr int m = decltype(m_)::value, ks = decltype(ks_)::value, LIVE = decltype(live_)::value;
@@ -181,7 +184,7 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[ks][j], A8 ? part[h] : fa[ks][i], acc[i][j], 4, A8 ? 0 : 4, 2 * ks,
                                                                   (int)sb[j], 2 * ks, (int)sa[i]);
       if constexpr (A8) {
-        __builtin_amdgcn_sched_barrier(0);
+        if (FIXED) __builtin_amdgcn_sched_barrier(0);
         constexpr int n = (i + 1) % LIVE;
 #pragma unroll
         for (int q = 8 * j / FN; q < 8 * (j + 1) / FN; ++q) {
@@ -237,7 +240,7 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
 #pragma unroll
           for (int r = m * NR * 2 / NM; r < (m + 1) * NR * 2 / NM && r < NR; ++r) read(r, 1, slot);
           each<l1 - l0>([&](auto i) { load(std::integral_constant<int, l0 + decltype(i)::value>(), lds0 + last); });
-          __builtin_amdgcn_sched_barrier(0);
+          if (FIXED) __builtin_amdgcn_sched_barrier(0);
         });
         advance();
         if (kt + S >= KT) none();
@@ -256,7 +259,7 @@ __device__ __forceinline__ void mx_tile(uint8_t* smem, const MxOperand& a, const
               read(r - FM - FN, 0, next);
           }
           each<l1 - l0>([&](auto i) { load(std::integral_constant<int, l0 + decltype(i)::value>(), lds0 + slot); });
-          __builtin_amdgcn_sched_barrier(0);
+          if (FIXED) __builtin_amdgcn_sched_barrier(0);
         });
         take_scales();
         last = slot;
@@ -846,7 +849,7 @@ hipError_t launch(bool wgrad, const GroupedMxParams& p, int ncu, hipStream_t st)
   // x 8192, 200 rows 7.3, 17.1; 32 experts of 300 x 7168, 3 rows each 10.8, 15.5. With more blocks a strip's own cost weighs more: 16
   // experts of 2816 x 2048, 32 rows each 13.8, 12.2; 256 experts, 1 row each 212, 161.
   // E4M3 rows, whose instructions cost twice as much, share a long contraction out further (us, in tiles): 16 experts of 2816 x 2048, 3
-  // rows each 12.6, 14.4, 32 rows each 18.0, 14.6; 256 rows of 4096 x 4096 16.3, 26.7, of 8192 x 8192 58, 49; and with few rows to an
+  // rows each 12.6, 14.4, 32 rows each 18.0, 14.6; 256 rows of 4096 x 4096 16.3, 26.7, of 8192 x 8192 58, 44; and with few rows to an
   // expert still further: 64 experts, 3 rows each 45.8, 67, 16 rows each 68.7, 68.4; 2048 x 1408, 4 rows each 28.5, 32.2, of 1024
   // x 512 11.6, 10.5; but 256 experts of 2048 x 1408 with 2 rows each 157, 81, as blocks without rows cost too.
   const int64_t fct = (p.N + FC - 1) / FC, frt = p.M / FR + met, fs = frt * ((p.N + 127) / 128);
